@@ -11,3 +11,7 @@ from .binding import (  # noqa: F401
     conv2d_plan_info, conv2d_status_string, conv2d_wgrad, conv2d_workspace_size, dgrad, fprop,
     load, problem_from, wgrad, workspace_for,
 )
+from .sequence import (  # noqa: F401
+    causal_conv, causal_conv_grad, causal_conv_step, selective_scan, selective_scan_grad,
+    selective_scan_step,
+)

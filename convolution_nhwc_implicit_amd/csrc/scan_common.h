@@ -1,0 +1,265 @@
+// scan_common.h -- what the forward and the gradient kernels of the selective
+// scan share: the wave's layout, token loads, chunk lookup and cross-lane sums.
+//
+// Layout of a wave: 16 channels, 4 lanes each (lane = 4 * channel + part).
+// Lane `part` holds NL neighbouring states of its channel, part*NL ..
+// part*NL+NL-1 (n <= 4*NL; states past n have A = B = C = 0 and stay 0).  What
+// belongs to a token and a channel but not to a state (step size, input, gate)
+// is computed once: of every four tokens lane `part` takes token `part`, and
+// the others read it through a quad broadcast.
+#pragma once
+
+#include "seq_internal.h"
+
+namespace cnv {
+
+template <int Q>
+__device__ inline float quad_bcast(float v)
+{
+    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), Q * 0x55, 0xf, 0xf, true));
+}
+template <int CTRL>
+__device__ inline float dpp(float v)
+{
+    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+}
+constexpr int kQuadXor1 = 0xb1, kQuadXor2 = 0x4e, kRowRor4 = 0x124, kRowRor8 = 0x128;
+
+// Sums over the four lanes of a quad of four values; lane q gets the sum of vq.
+__device__ inline float quad_scatter_sum(float v0, float v1, float v2, float v3, bool odd, bool high)
+{
+    const float a = (odd ? v1 : v0) + dpp<kQuadXor1>(odd ? v0 : v1);
+    const float b = (odd ? v3 : v2) + dpp<kQuadXor1>(odd ? v2 : v3);
+    return (high ? b : a) + dpp<kQuadXor2>(high ? a : b);
+}
+
+// Sum over the quad of one value, in every lane.
+__device__ inline float quad_sum(float v)
+{
+    v += dpp<kQuadXor1>(v);
+    return v + dpp<kQuadXor2>(v);
+}
+
+// Sums of four values over the wave's 16 channels (lanes with the same
+// lane % 4).  Row r of 16 lanes gets the sum of vr, in each of its quads.
+__device__ inline float channel_sum4(float v0, float v1, float v2, float v3)
+{
+    // the builtins' two results, as values first: a bit cast of a vector's element reads element 0
+    auto half = [](float a, float b) {
+        const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(unsigned, a), __builtin_bit_cast(unsigned, b),
+                                                        false, false);
+        const unsigned u = r[0], v = r[1];
+        return __builtin_bit_cast(float, u) + __builtin_bit_cast(float, v);
+    };
+    const float s01 = half(v0, v1), s23 = half(v2, v3);
+    const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(unsigned, s01), __builtin_bit_cast(unsigned, s23),
+                                                    false, false);
+    const unsigned lo = r[0], hi = r[1];
+    float s = __builtin_bit_cast(float, lo) + __builtin_bit_cast(float, hi);
+    s += dpp<kRowRor4>(s);
+    return s + dpp<kRowRor8>(s);
+}
+
+// log(1 + e^raw) = max(raw, 0) + log1p(e), e = e^-|raw| in (0, 1].  With
+// w = e / (2 + e) <= 1/3, log1p(e) = 2 atanh(w) = 2 w (1 + w^2/3 + w^4/5 + ...):
+// relative accuracy for every raw (1 + e would lose small e's bits); the first
+// term left out is below 2^-27 of the sum.
+__device__ inline float softplus_f32(float raw)
+{
+    const float e = __builtin_amdgcn_exp2f(-kLog2e * __builtin_fabsf(raw));
+    const float w = e * __builtin_amdgcn_rcpf(2.0f + e), s = w * w;
+    float p = 1.0f / 15.0f;
+    p = __builtin_fmaf(p, s, 1.0f / 13.0f);
+    p = __builtin_fmaf(p, s, 1.0f / 11.0f);
+    p = __builtin_fmaf(p, s, 1.0f / 9.0f);
+    p = __builtin_fmaf(p, s, 1.0f / 7.0f);
+    p = __builtin_fmaf(p, s, 1.0f / 5.0f);
+    p = __builtin_fmaf(p, s, 1.0f / 3.0f);
+    p = __builtin_fmaf(p, s, 1.0f);
+    const float r = __builtin_fmaf(2.0f * w, p, __builtin_fmaxf(raw, 0.0f));
+    return raw != raw ? raw : r;  // the maximum above drops a NaN
+}
+
+// The chunk that a workgroup walks.
+struct Chunk {
+    int s;            // sequence
+    bool first, last; // of its sequence
+    long long t0, t1; // its rows
+    bool valid;
+};
+
+__device__ inline int chunks_of(const ScanArgs &a, int s)
+{
+    const long long len = a.q.end(s) - a.q.begin(s);
+    const long long c = (len + a.chunk - 1) / a.chunk;
+    return c < 1 ? 1 : (int)c;  // an empty sequence still passes its state on
+}
+
+// Slot -> chunk.  Packed: sequences' chunks lie in order, 64 sequences looked
+// at together, a lane each.
+__device__ inline Chunk find_chunk(const ScanArgs &a, int slot)
+{
+    Chunk r;
+    int c = 0, count = a.chunks;
+    r.valid = true;
+    if (!a.q.start) {
+        r.s = slot / a.chunks;
+        c = slot % a.chunks;
+    } else {
+        const int lane = threadIdx.x % 64;
+        int base = 0;
+        r.valid = false;
+        for (int s0 = 0; s0 < a.q.seqs && !r.valid; s0 += 64) {
+            const int mine = s0 + lane < a.q.seqs ? chunks_of(a, s0 + lane) : 0;
+            int incl = mine;
+            for (int o = 1; o < 64; o <<= 1) {
+                const int v = __shfl_up(incl, o);
+                if (lane >= o) incl += v;
+            }
+            const unsigned long long past = __ballot(base + incl > slot);
+            if (past) {
+                const int at = __builtin_ctzll(past);
+                r.s = s0 + at;
+                count = __shfl(mine, at);
+                c = slot - (base + __shfl(incl, at) - count);
+                r.valid = true;
+            }
+            base += __shfl(incl, 63);
+        }
+        if (!r.valid) return r;
+        r.s = __builtin_amdgcn_readfirstlane(r.s);
+        c = __builtin_amdgcn_readfirstlane(c);
+        count = __builtin_amdgcn_readfirstlane(count);
+    }
+    r.first = c == 0;
+    r.last = c == count - 1;
+    const long long b = a.q.begin(r.s), e = a.q.end(r.s);
+    r.t0 = b + (long long)c * a.chunk;
+    r.t1 = r.t0 + a.chunk < e ? r.t0 + a.chunk : e;
+    if (r.t1 < r.t0) r.t1 = r.t0;
+    return r;
+}
+
+// Where the state before the step at row t of a chunk is kept.  Neighbouring
+// chunks' ranges do not meet: each has one entry more than the whole steps
+// between its first row and the next chunk's.  Never past tokens/TS + slots.
+template <int TS>
+__device__ inline long long scan_keep_index(const Chunk &k, int slot, long long t)
+{
+    return k.t0 / TS + slot + (t - k.t0) / TS;
+}
+
+// The channels of a workgroup and a lane.
+struct Channels {
+    int group, block;  // group of B and C, channel block over all groups
+    int ch;            // this lane's channel, clamped to one that exists
+    bool valid;        // whether it exists
+    int part;          // lane % 4
+    __device__ inline Channels(const ScanArgs &a, int blk)
+    {
+        const int dg = a.d / a.groups, lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+        block = blk;
+        group = blk / a.blocks_per_group;
+        const int c = (blk % a.blocks_per_group) * kScanChannels + wave * 16 + lane / 4;
+        valid = c < dg;
+        ch = group * dg + (valid ? c : dg - 1);
+        part = lane % 4;
+    }
+};
+
+// A lane's values of one step of TS tokens: token 4*i + part for i < TS/4.
+// Rows past the chunk are read from its last row and given no weight by the
+// caller.  base: the tensor's row t of the step, lane offset included.
+template <int TS>
+struct Rows {
+    uint32_t off[TS / 4];
+    __device__ inline void set(long long row, int ch, int part, long long rem)
+    {
+#pragma unroll
+        for (int i = 0; i < TS / 4; ++i) {
+            const int t = 4 * i + part;
+            const uint32_t r = (uint32_t)(t < rem ? t : (int)rem - 1);
+            off[i] = r * (uint32_t)row + (uint32_t)ch;
+        }
+    }
+};
+
+// B and C of a step as fp32 in LDS, [TS][4*NL].  Thread i of the workgroup
+// takes value i (TS * 4*NL <= 256).
+template <class E, int NL, int TS>
+struct StageBC {
+    static constexpr int kCount = TS * 4 * NL;
+    float b, c;
+    __device__ inline void load(const ScanArgs &a, const Chunk &k, int group, long long t, bool want_c)
+    {
+        b = c = 0.0f;
+        const int tid = threadIdx.x;
+        if (tid >= kCount) return;
+        const long long tt = t + tid / (4 * NL);
+        const int n = tid % (4 * NL);
+        if (n < a.n && tt < k.t1) {
+            b = E::to(((const typename E::S *)a.B)[a.bs.at(a.q, k.s, tt) + group * a.b_group + n]);
+            if (want_c) c = E::to(((const typename E::S *)a.C)[a.cs.at(a.q, k.s, tt) + group * a.c_group + n]);
+        }
+    }
+    __device__ inline void store(float *lb, float *lc) const
+    {
+        if (threadIdx.x < kCount) {
+            lb[threadIdx.x] = b;
+            if (lc) lc[threadIdx.x] = c;
+        }
+    }
+};
+
+template <int NL>
+__device__ inline void load_states(const float *p, float (&v)[NL])
+{
+#pragma unroll
+    for (int j = 0; j < NL; ++j) v[j] = p[j];
+}
+
+// NL states of a lane in an [..][d][n] array; n may be short of 4*NL.
+template <int NL>
+__device__ inline void read_nl(const float *p, int n, int part, float (&v)[NL])
+{
+    if (n == 4 * NL) {
+        const SVec<float, NL> r = *(const SVec<float, NL> *)(p + part * NL);
+#pragma unroll
+        for (int j = 0; j < NL; ++j) v[j] = r.v[j];
+    } else {
+#pragma unroll
+        for (int j = 0; j < NL; ++j) v[j] = part * NL + j < n ? p[part * NL + j] : 0.0f;
+    }
+}
+template <int NL>
+__device__ inline void write_nl(float *p, int n, int part, const float (&v)[NL])
+{
+    if (n == 4 * NL) {
+        SVec<float, NL> r;
+#pragma unroll
+        for (int j = 0; j < NL; ++j) r.v[j] = v[j];
+        *(SVec<float, NL> *)(p + part * NL) = r;
+    } else {
+#pragma unroll
+        for (int j = 0; j < NL; ++j)
+            if (part * NL + j < n) p[part * NL + j] = v[j];
+    }
+}
+
+// f(element type, NL as a constant) for the smallest NL with 4 * NL >= n
+template <class F>
+hipError_t scan_by_type(int dtype, int n, F f)
+{
+    auto states = [&](auto e) {
+        if (n <= 4) return f(e, std::integral_constant<int, 1>{});
+        if (n <= 8) return f(e, std::integral_constant<int, 2>{});
+        if (n <= 16) return f(e, std::integral_constant<int, 4>{});
+        if (n <= 32) return f(e, std::integral_constant<int, 8>{});
+        return f(e, std::integral_constant<int, 16>{});
+    };
+    if (dtype == CONV2D_DTYPE_F16) return states(SF16{});
+    if (dtype == CONV2D_DTYPE_BF16) return states(SBF16{});
+    return states(SF32{});
+}
+
+}  // namespace cnv

@@ -1,0 +1,252 @@
+// selective_scan.hip -- the selective scan forward, and its single-token step.
+//
+//   delta = softplus(dt + dt_bias)
+//   h[t][c][n] = exp(delta[t][c] A[c][n]) h[t-1][c][n] + delta[t][c] x[t][c] B[t][g(c)][n]
+//   y[t][c] = (sum_n h[t][c][n] C[t][g(c)][n] + D[c] x[t][c]) silu(z[t][c])
+//
+// States stay in fp32 registers; only inputs and outputs cross memory.  Every
+// (t, c, n) costs one exp2 (8 cycles of a wave64) and four plain operations (4
+// each), which outweighs the bytes: the kernels are bound by the vector units.
+#include "scan_common.h"
+
+namespace cnv {
+namespace {
+
+// One chunk of one sequence for 64 channels.  LOCAL: from a zero state, only
+// the state the chunk ends with and the sum of its steps are written (the
+// decay over a chunk is exp(A * that sum)), for scan_join_kernel.
+template <class E, int NL, bool LOCAL>
+__global__ __launch_bounds__(256) void scan_kernel(ScanArgs a)
+{
+    constexpr int TS = scan_step_tokens(4 * NL), G = TS / 4;
+    using S = typename E::S;
+    const int slot = blockIdx.x;
+    const Chunk k = find_chunk(a, slot);
+    if (!k.valid || (LOCAL && k.last)) return;
+    const Channels c(a, blockIdx.y);
+    const int part = c.part;
+    const bool odd = part & 1, high = part & 2;
+
+    float A2[NL], h[NL];
+    read_nl<NL>(a.A + (long long)c.ch * a.n, a.n, part, A2);
+#pragma unroll
+    for (int j = 0; j < NL; ++j) {
+        A2[j] *= kLog2e;
+        h[j] = 0.0f;
+    }
+    if (!LOCAL) {
+        if (a.chunk_state) read_nl<NL>(a.chunk_state + ((long long)slot * a.d + c.ch) * a.n, a.n, part, h);
+        else if (a.initial) read_nl<NL>(a.initial + ((long long)k.s * a.d + c.ch) * a.n, a.n, part, h);
+    }
+    const float bias = a.dt_bias ? a.dt_bias[c.ch] : 0.0f, D = !LOCAL && a.D ? a.D[c.ch] : 0.0f;
+    float sum_delta = 0.0f;
+
+    __shared__ float lb[2][TS * 4 * NL], lc[2][TS * 4 * NL];
+    Rows<TS> rx, rdt, rz, ry;
+    S x[G], dt[G], z[G];
+    StageBC<E, NL, TS> bc;
+    auto offsets = [&](long long rem) {
+        rx.set(a.xs.row, c.ch, part, rem);
+        rdt.set(a.dts.row, c.ch, part, rem);
+        if (!LOCAL) ry.set(a.d, c.ch, part, rem);
+        if (!LOCAL && a.z) rz.set(a.zs.row, c.ch, part, rem);
+    };
+    auto fetch = [&](long long t) {
+        const S *px = (const S *)a.x + a.xs.at(a.q, k.s, t), *pdt = (const S *)a.dt + a.dts.at(a.q, k.s, t);
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+            x[i] = px[rx.off[i]];
+            dt[i] = pdt[rdt.off[i]];
+        }
+        if (!LOCAL && a.z) {
+            const S *pz = (const S *)a.z + a.zs.at(a.q, k.s, t);
+#pragma unroll
+            for (int i = 0; i < G; ++i) z[i] = pz[rz.off[i]];
+        }
+        bc.load(a, k, c.group, t, !LOCAL);
+    };
+    if (k.t0 < k.t1) {
+        offsets(k.t1 - k.t0);
+        fetch(k.t0);
+    }
+    int buf = 0;
+    for (long long t = k.t0; t < k.t1; t += TS, buf ^= 1) {
+        const long long rem = k.t1 - t;
+        float delta[G], dx[G], xv[G], zv[G];
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+            const bool valid = c.valid && 4 * i + part < rem;
+            const float raw = E::to(dt[i]) + bias;
+            xv[i] = E::to(x[i]);
+            delta[i] = a.softplus ? softplus_f32(raw) : raw;
+            dx[i] = valid ? delta[i] * xv[i] : 0.0f;
+            delta[i] = valid ? delta[i] : 0.0f;  // a token that is not there leaves the state as it is
+            if (LOCAL) sum_delta += delta[i];
+            if (!LOCAL) zv[i] = a.z ? E::to(z[i]) : 0.0f;
+        }
+        bc.store(lb[buf], LOCAL ? nullptr : lc[buf]);
+        uint32_t yoff[G];
+#pragma unroll
+        for (int i = 0; i < G; ++i) yoff[i] = LOCAL ? 0 : ry.off[i];
+        if (rem > TS) {
+            if (rem < 2 * TS) offsets(rem - TS);
+            fetch(t + TS);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+            float acc[4];
+            auto token = [&](auto qc) {
+                constexpr int Q = decltype(qc)::value;
+                const float *pb = &lb[buf][(4 * i + Q) * 4 * NL + part * NL], *pc = &lc[buf][(4 * i + Q) * 4 * NL + part * NL];
+                const float dq = quad_bcast<Q>(delta[i]), dxq = quad_bcast<Q>(dx[i]);
+                float v = 0.0f;
+#pragma unroll
+                for (int j = 0; j < NL; ++j) {
+                    h[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(dq * A2[j]), h[j], dxq * pb[j]);
+                    if (!LOCAL) v = __builtin_fmaf(h[j], pc[j], v);
+                }
+                acc[Q] = v;
+            };
+            token(std::integral_constant<int, 0>{});
+            token(std::integral_constant<int, 1>{});
+            token(std::integral_constant<int, 2>{});
+            token(std::integral_constant<int, 3>{});
+            if (!LOCAL) {
+                float v = __builtin_fmaf(D, xv[i], quad_scatter_sum(acc[0], acc[1], acc[2], acc[3], odd, high));
+                if (a.z) v *= zv[i] * sigmoid_f32(zv[i]);
+                if (c.valid && 4 * i + part < rem) ((S *)a.y + t * a.d)[yoff[i]] = E::from(v);
+            }
+        }
+    }
+    if (LOCAL) {
+        if (!c.valid) return;
+        write_nl<NL>(a.chunk_state + ((long long)slot * a.d + c.ch) * a.n, a.n, part, h);
+        sum_delta = quad_sum(sum_delta);
+        if (part == 0) a.chunk_delta[(long long)slot * a.d + c.ch] = sum_delta;
+    } else if (a.final_state && k.last && c.valid) {
+        write_nl<NL>(a.final_state + ((long long)k.s * a.d + c.ch) * a.n, a.n, part, h);
+    }
+}
+
+// Turns the chunks' own end states into the states they start with, one thread
+// to a (sequence, channel, state).  With chunk_back the gradient's carries are
+// joined the same way from the last chunk back: what a chunk hands back from
+// its own tokens becomes what it gets from the chunks after it.
+__global__ __launch_bounds__(256) void scan_join_kernel(ScanArgs a)
+{
+    const int s = blockIdx.x;
+    int first = 0, count = a.chunks;
+    if (!a.q.start) {
+        first = s * a.chunks;
+    } else {
+        const int lane = threadIdx.x % 64;
+        for (int s0 = 0; s0 < s; s0 += 64) {
+            int v = s0 + lane < s ? chunks_of(a, s0 + lane) : 0;
+            for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
+            first += v;
+        }
+        first = __builtin_amdgcn_readfirstlane(first);
+        count = chunks_of(a, s);
+    }
+    if (count > a.slots - first) count = a.slots - first;  // only if seq_start descends somewhere
+    const long long i = (long long)blockIdx.y * 256 + threadIdx.x, per = (long long)a.d * a.n;
+    if (i >= per) return;
+    const long long ch = i / a.n;
+    const float A2 = a.A[i] * kLog2e;
+    float h = a.initial ? a.initial[s * per + i] : 0.0f;
+    for (int c = 0; c < count; ++c) {
+        float *p = a.chunk_state + (first + c) * per + i;
+        const float own = *p;
+        *p = h;
+        if (c + 1 < count) h = __builtin_fmaf(__builtin_amdgcn_exp2f(A2 * a.chunk_delta[(long long)(first + c) * a.d + ch]), h, own);
+    }
+    if (!a.chunk_back) return;
+    float b = a.dfinal ? a.dfinal[s * per + i] : 0.0f;
+    for (int c = count - 1; c >= 0; --c) {
+        float *p = a.chunk_back + (first + c) * per + i;
+        const float own = *p;
+        *p = b;
+        b = __builtin_fmaf(__builtin_amdgcn_exp2f(A2 * a.chunk_delta[(long long)(first + c) * a.d + ch]), b, own);
+    }
+    if (a.dinitial) a.dinitial[s * per + i] = b;
+}
+
+// One token per row on pooled states: 4 lanes to a channel as above.
+template <class E, int NL>
+__global__ __launch_bounds__(256) void scan_step_kernel(ScanStepArgs a)
+{
+    using S = typename E::S;
+    const int part = threadIdx.x % 4, ch = blockIdx.y * 64 + threadIdx.x / 4;
+    const long long r = blockIdx.x;
+    if (ch >= a.d) return;
+    const int slot = a.slots ? a.slots[r] : (int)r;
+    S *y = (S *)a.y + r * a.d + ch;
+    if (slot < 0 || slot >= a.pool) {
+        if (part == 0) *y = E::from(0.0f);
+        return;
+    }
+    const int group = ch / (a.d / a.groups);
+    float A[NL], h[NL];
+    float *state = a.state + ((long long)slot * a.d + ch) * a.n;
+    read_nl<NL>(state, a.n, part, h);
+    read_nl<NL>(a.A + (long long)ch * a.n, a.n, part, A);
+    const float x = E::to(((const S *)a.x)[r * a.x_row + ch]);
+    const float raw = E::to(((const S *)a.dt)[r * a.dt_row + ch]) + (a.dt_bias ? a.dt_bias[ch] : 0.0f);
+    const float delta = a.softplus ? softplus_f32(raw) : raw, dx = delta * x;
+    float v = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NL; ++j) {
+        const int n = part * NL + j;
+        if (n < a.n) {
+            const float B = E::to(((const S *)a.B)[r * a.b_row + group * a.b_group + n]);
+            const float C = E::to(((const S *)a.C)[r * a.c_row + group * a.c_group + n]);
+            h[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(delta * (A[j] * kLog2e)), h[j], dx * B);
+            v = __builtin_fmaf(h[j], C, v);
+        }
+    }
+    write_nl<NL>(state, a.n, part, h);
+    v = quad_sum(v);
+    if (part != 0) return;
+    if (a.D) v = __builtin_fmaf(a.D[ch], x, v);
+    if (a.z) {
+        const float z = E::to(((const S *)a.z)[r * a.z_row + ch]);
+        v *= z * sigmoid_f32(z);
+    }
+    *y = E::from(v);
+}
+
+}  // namespace
+
+void launch_scan_join(const ScanArgs &a, hipStream_t st)
+{
+    const long long per = (long long)a.d * a.n;
+    scan_join_kernel<<<dim3((unsigned)a.q.seqs, (unsigned)((per + 255) / 256)), 256, 0, st>>>(a);
+}
+
+hipError_t launch_scan(int dtype, const ScanArgs &a, hipStream_t st)
+{
+    const dim3 grid((unsigned)a.slots, (unsigned)(a.blocks_per_group * a.groups));
+    return scan_by_type(dtype, a.n, [&](auto e, auto nl) {
+        using E = decltype(e);
+        constexpr int NL = decltype(nl)::value;
+        if (a.chunk_state) {
+            scan_kernel<E, NL, true><<<grid, 256, 0, st>>>(a);
+            launch_scan_join(a, st);
+        }
+        scan_kernel<E, NL, false><<<grid, 256, 0, st>>>(a);
+        return hipGetLastError();
+    });
+}
+
+hipError_t launch_scan_step(int dtype, const ScanStepArgs &a, hipStream_t st)
+{
+    const dim3 grid((unsigned)a.rows, (unsigned)((a.d + 63) / 64));
+    return scan_by_type(dtype, a.n, [&](auto e, auto nl) {
+        using E = decltype(e);
+        scan_step_kernel<E, decltype(nl)::value><<<grid, 256, 0, st>>>(a);
+        return hipGetLastError();
+    });
+}
+
+}  // namespace cnv

@@ -1,0 +1,399 @@
+// selective_scan_grad.hip -- gradients of the selective scan.
+//
+// With the output gradient through the gate g[t] = dy[t] silu(z[t]) and
+// a[t] = exp(delta[t] A), the states' gradients run backwards,
+//   dh[t] = g[t] C[t] + a[t+1] dh[t+1],
+// and give, with k[t] = a[t] dh[t] (what goes on to token t-1),
+//   dC[t] = sum_c g[t] h[t]                 dB[t] = sum_c delta[t] x[t] dh[t]
+//   inner[t] = sum_n dh[t] B[t]             du[t] = delta[t] inner[t] + D g[t]
+//   ddelta[t] = x[t] inner[t] + sum_n k[t] h[t-1] A
+//   dA = sum_t k[t] h[t-1] delta[t]         dD = sum_t g[t] x[t]
+//   ddt = ddelta softplus'(dt + dt_bias)    dz = dy y_before_gate silu'(z)
+// where c runs over the channels of a group.
+//
+// Three kernels.  The first walks each chunk forwards and keeps the state before
+// every step of TS tokens; where sequences are cut into chunks it starts them
+// from zero, and adds up what the chunk's own tokens hand back to the tokens
+// before it, sum_t (a[0] .. a[t]) g[t] C[t], so that scan_join_kernel can give
+// every chunk both its first state and its last carry.  The second walks each
+// chunk backwards, a step at a time: the step's states and decays are computed
+// again from the kept state into registers (TS * NL values of each), so that the
+// backward walk needs no further exponential.  The last adds up the partial sums
+// of dA, dB, dC, dD and ddt_bias in a fixed order.
+#include "scan_common.h"
+
+namespace cnv {
+
+void launch_scan_join(const ScanArgs &a, hipStream_t st);
+
+namespace {
+
+// What a step's tokens read, as stored.
+template <class E, int G>
+struct Tokens {
+    typename E::S x[G], dt[G], z[G], dy[G];
+};
+
+template <int TS>
+struct TokenRows {
+    Rows<TS> x, dt, z, dy;
+    __device__ inline void set(const ScanArgs &a, int ch, int part, long long rem)
+    {
+        x.set(a.xs.row, ch, part, rem);
+        dt.set(a.dts.row, ch, part, rem);
+        if (a.z) z.set(a.zs.row, ch, part, rem);
+        dy.set(a.dys.row, ch, part, rem);
+    }
+};
+
+template <class E, int TS, bool GRAD>
+__device__ inline void fetch_tokens(const ScanArgs &a, const Chunk &k, long long t, const TokenRows<TS> &r, Tokens<E, TS / 4> &o)
+{
+    using S = typename E::S;
+    const S *px = (const S *)a.x + a.xs.at(a.q, k.s, t), *pdt = (const S *)a.dt + a.dts.at(a.q, k.s, t);
+#pragma unroll
+    for (int i = 0; i < TS / 4; ++i) {
+        o.x[i] = px[r.x.off[i]];
+        o.dt[i] = pdt[r.dt.off[i]];
+    }
+    if (!GRAD) return;
+    const S *pdy = (const S *)a.dy + a.dys.at(a.q, k.s, t);
+#pragma unroll
+    for (int i = 0; i < TS / 4; ++i) o.dy[i] = pdy[r.dy.off[i]];
+    if (a.z) {
+        const S *pz = (const S *)a.z + a.zs.at(a.q, k.s, t);
+#pragma unroll
+        for (int i = 0; i < TS / 4; ++i) o.z[i] = pz[r.z.off[i]];
+    }
+}
+
+template <class E, int NL, bool CARRY>
+__global__ __launch_bounds__(256) void scan_keep_kernel(ScanArgs a)
+{
+    constexpr int TS = scan_step_tokens(4 * NL), G = TS / 4;
+    const int slot = blockIdx.x;
+    const Chunk k = find_chunk(a, slot);
+    if (!k.valid) return;
+    const Channels c(a, blockIdx.y);
+    const int part = c.part;
+    float A2[NL], h[NL], P[NL], back[NL];
+    read_nl<NL>(a.A + (long long)c.ch * a.n, a.n, part, A2);
+#pragma unroll
+    for (int j = 0; j < NL; ++j) {
+        A2[j] *= kLog2e;
+        h[j] = back[j] = 0.0f;
+        P[j] = 1.0f;
+    }
+    if (!CARRY && a.initial && c.valid) read_nl<NL>(a.initial + ((long long)k.s * a.d + c.ch) * a.n, a.n, part, h);
+    const float bias = a.dt_bias ? a.dt_bias[c.ch] : 0.0f;
+    float sum_delta = 0.0f;
+
+    __shared__ float lb[2][TS * 4 * NL], lc[2][TS * 4 * NL];
+    TokenRows<TS> rows;
+    Tokens<E, G> in;
+    StageBC<E, NL, TS> bc;
+    if (k.t0 < k.t1) {
+        rows.set(a, c.ch, part, k.t1 - k.t0);
+        fetch_tokens<E, TS, CARRY>(a, k, k.t0, rows, in);
+        bc.load(a, k, c.group, k.t0, CARRY);
+    }
+    int buf = 0;
+    long long keep = scan_keep_index<TS>(k, slot, k.t0) * a.d + c.ch;
+    for (long long t = k.t0; t < k.t1; t += TS, buf ^= 1, keep += a.d) {
+        const long long rem = k.t1 - t;
+        float delta[G], dx[G], g[G], step_delta = 0.0f;
+        if (c.valid) write_nl<NL>(a.check + keep * a.n, a.n, part, h);
+        if (CARRY && c.valid && part == 0) a.check_delta[keep] = sum_delta;
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+            const bool valid = c.valid && 4 * i + part < rem;
+            const float raw = E::to(in.dt[i]) + bias;
+            delta[i] = a.softplus ? softplus_f32(raw) : raw;
+            dx[i] = valid ? delta[i] * E::to(in.x[i]) : 0.0f;
+            delta[i] = valid ? delta[i] : 0.0f;
+            step_delta += delta[i];
+            g[i] = 0.0f;
+            if (CARRY) {
+                g[i] = E::to(in.dy[i]);
+                if (a.z) {
+                    const float z = E::to(in.z[i]);
+                    g[i] *= z * sigmoid_f32(z);
+                }
+                g[i] = valid ? g[i] : 0.0f;
+            }
+        }
+        if (CARRY) sum_delta += quad_sum(step_delta);
+        bc.store(lb[buf], CARRY ? lc[buf] : nullptr);
+        if (rem > TS) {
+            if (rem < 2 * TS) rows.set(a, c.ch, part, rem - TS);
+            fetch_tokens<E, TS, CARRY>(a, k, t + TS, rows, in);
+            bc.load(a, k, c.group, t + TS, CARRY);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+            auto token = [&](auto qc) {
+                constexpr int Q = decltype(qc)::value;
+                const float *pb = &lb[buf][(4 * i + Q) * 4 * NL + part * NL], *pc = &lc[buf][(4 * i + Q) * 4 * NL + part * NL];
+                const float dq = quad_bcast<Q>(delta[i]), dxq = quad_bcast<Q>(dx[i]), gq = quad_bcast<Q>(g[i]);
+#pragma unroll
+                for (int j = 0; j < NL; ++j) {
+                    const float e = __builtin_amdgcn_exp2f(dq * A2[j]);
+                    h[j] = __builtin_fmaf(e, h[j], dxq * pb[j]);
+                    if (CARRY) {
+                        P[j] *= e;
+                        back[j] = __builtin_fmaf(P[j], gq * pc[j], back[j]);
+                    }
+                }
+            };
+            token(std::integral_constant<int, 0>{});
+            token(std::integral_constant<int, 1>{});
+            token(std::integral_constant<int, 2>{});
+            token(std::integral_constant<int, 3>{});
+        }
+    }
+    if (CARRY && c.valid) {
+        const long long at = (long long)slot * a.d + c.ch;
+        write_nl<NL>(a.chunk_state + at * a.n, a.n, part, h);
+        write_nl<NL>(a.chunk_back + at * a.n, a.n, part, back);
+        if (part == 0) a.chunk_delta[at] = sum_delta;
+    }
+}
+
+template <class E, int NL>
+__global__ __launch_bounds__(256, 2) void scan_back_kernel(ScanArgs a)
+{
+    constexpr int TS = scan_step_tokens(4 * NL), G = TS / 4, N4 = 4 * NL;
+    using S = typename E::S;
+    const int slot = blockIdx.x, tid = threadIdx.x;
+    const Chunk k = find_chunk(a, slot);
+    const Channels c(a, blockIdx.y);
+    const int part = c.part, row = tid % 64 / 16, wave = tid / 64;
+    const bool odd = part & 1, high = part & 2;
+    const long long at = (long long)slot * a.d + c.ch;
+    float A[NL], carry[NL], H0[NL], dA[NL], sum_D = 0.0f, sum_bias = 0.0f;
+    read_nl<NL>(a.A + (long long)c.ch * a.n, a.n, part, A);
+#pragma unroll
+    for (int j = 0; j < NL; ++j) dA[j] = carry[j] = H0[j] = 0.0f;
+    const bool joined = a.chunk_state != nullptr;
+    if (k.valid && c.valid) {
+        if (joined) {
+            read_nl<NL>(a.chunk_back + at * a.n, a.n, part, carry);
+            read_nl<NL>(a.chunk_state + at * a.n, a.n, part, H0);
+        } else if (a.dfinal) {
+            read_nl<NL>(a.dfinal + ((long long)k.s * a.d + c.ch) * a.n, a.n, part, carry);
+        }
+    }
+    const float bias = a.dt_bias ? a.dt_bias[c.ch] : 0.0f, D = a.D ? a.D[c.ch] : 0.0f;
+
+    __shared__ float lb[TS * N4], lc[TS * N4];
+    __shared__ float sb[4][TS * N4], sc[4][TS * N4];  // the waves' sums of dB and dC
+    TokenRows<TS> rows;
+    Tokens<E, G> in;
+    StageBC<E, NL, TS> bc;
+    float kept[NL], kept_delta = 0.0f;
+    auto fetch = [&](long long t) {
+        fetch_tokens<E, TS, true>(a, k, t, rows, in);
+        bc.load(a, k, c.group, t, true);
+        const long long keep = scan_keep_index<TS>(k, slot, t) * a.d + c.ch;
+        read_nl<NL>(a.check + keep * a.n, a.n, part, kept);
+        if (joined) kept_delta = a.check_delta[keep];
+    };
+    const long long len = k.valid ? k.t1 - k.t0 : 0;
+    long long t = k.t0 + (len - 1) / TS * TS;  // the last step, perhaps short
+    if (len > 0) {
+        rows.set(a, c.ch, part, k.t1 - t);
+        fetch(t);
+    }
+    for (long long left = (len + TS - 1) / TS; left > 0; --left, t -= TS) {
+        const long long rem = k.t1 - t < TS ? k.t1 - t : TS;
+        float delta[G], dx[G], xv[G], g[G], dyv[G], zv[G], sig_raw[G], h0[NL];
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+            const bool valid = c.valid && 4 * i + part < rem;
+            const float raw = E::to(in.dt[i]) + bias;
+            xv[i] = E::to(in.x[i]);
+            delta[i] = a.softplus ? softplus_f32(raw) : raw;
+            sig_raw[i] = a.softplus ? sigmoid_f32(raw) : 1.0f;
+            dx[i] = valid ? delta[i] * xv[i] : 0.0f;
+            delta[i] = valid ? delta[i] : 0.0f;
+            dyv[i] = E::to(in.dy[i]);
+            zv[i] = a.z ? E::to(in.z[i]) : 0.0f;
+            g[i] = a.z ? dyv[i] * (zv[i] * sigmoid_f32(zv[i])) : dyv[i];
+            g[i] = valid ? g[i] : 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < NL; ++j) {
+            h0[j] = c.valid ? kept[j] : 0.0f;
+            if (joined) h0[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(kept_delta * (A[j] * kLog2e)), H0[j], h0[j]);
+        }
+        bc.store(lb, lc);
+        if (left > 1) {
+            if (rem < TS) rows.set(a, c.ch, part, TS);
+            fetch(t - TS);
+        }
+        __syncthreads();
+
+        float e[TS][NL], h[TS][NL], ys[G];
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+            float acc[4];
+            auto token = [&](auto qc) {
+                constexpr int Q = decltype(qc)::value;
+                const int u = 4 * i + Q;
+                const float dq = quad_bcast<Q>(delta[i]), dxq = quad_bcast<Q>(dx[i]);
+                float v = 0.0f;
+#pragma unroll
+                for (int j = 0; j < NL; ++j) {
+                    e[u][j] = __builtin_amdgcn_exp2f(dq * (A[j] * kLog2e));
+                    h[u][j] = __builtin_fmaf(e[u][j], u ? h[u - 1][j] : h0[j], dxq * lb[u * N4 + part * NL + j]);
+                    v = __builtin_fmaf(h[u][j], lc[u * N4 + part * NL + j], v);
+                }
+                acc[Q] = v;
+            };
+            token(std::integral_constant<int, 0>{});
+            token(std::integral_constant<int, 1>{});
+            token(std::integral_constant<int, 2>{});
+            token(std::integral_constant<int, 3>{});
+            ys[i] = quad_scatter_sum(acc[0], acc[1], acc[2], acc[3], odd, high);
+        }
+#pragma unroll
+        for (int i = G - 1; i >= 0; --i) {
+            float inner[4], along[4], vb[NL][4], vc[NL][4];
+            auto token = [&](auto qc) {
+                constexpr int Q = decltype(qc)::value;
+                const int u = 4 * i + Q;
+                const float dq = quad_bcast<Q>(delta[i]), dxq = quad_bcast<Q>(dx[i]), gq = quad_bcast<Q>(g[i]);
+                inner[Q] = along[Q] = 0.0f;
+#pragma unroll
+                for (int j = 0; j < NL; ++j) {
+                    const float dh = __builtin_fmaf(gq, lc[u * N4 + part * NL + j], carry[j]);
+                    vc[j][Q] = gq * h[u][j];
+                    vb[j][Q] = dxq * dh;
+                    inner[Q] = __builtin_fmaf(dh, lb[u * N4 + part * NL + j], inner[Q]);
+                    carry[j] = dh * e[u][j];
+                    const float b = carry[j] * (u ? h[u - 1][j] : h0[j]);
+                    along[Q] = __builtin_fmaf(b, A[j], along[Q]);
+                    dA[j] = __builtin_fmaf(b, dq, dA[j]);
+                }
+            };
+            token(std::integral_constant<int, 3>{});
+            token(std::integral_constant<int, 2>{});
+            token(std::integral_constant<int, 1>{});
+            token(std::integral_constant<int, 0>{});
+#pragma unroll
+            for (int j = 0; j < NL; ++j) {
+                const float tb = channel_sum4(vb[j][0], vb[j][1], vb[j][2], vb[j][3]);
+                const float tc = channel_sum4(vc[j][0], vc[j][1], vc[j][2], vc[j][3]);
+                if (tid % 16 < 4) {
+                    sb[wave][(4 * i + row) * N4 + part * NL + j] = tb;
+                    sc[wave][(4 * i + row) * N4 + part * NL + j] = tc;
+                }
+            }
+            const float in_sum = quad_scatter_sum(inner[0], inner[1], inner[2], inner[3], odd, high);
+            const float al_sum = quad_scatter_sum(along[0], along[1], along[2], along[3], odd, high);
+            const bool valid = c.valid && 4 * i + part < rem;
+            if (valid) {
+                const long long o = (t + 4 * i + part) * a.d + c.ch;
+                const float draw = __builtin_fmaf(xv[i], in_sum, al_sum) * sig_raw[i];
+                sum_D = __builtin_fmaf(g[i], xv[i], sum_D);
+                sum_bias += draw;
+                ((S *)a.du)[o] = E::from(__builtin_fmaf(delta[i], in_sum, D * g[i]));
+                ((S *)a.ddt)[o] = E::from(draw);
+                if (a.z) {
+                    const float sg = sigmoid_f32(zv[i]), yv = __builtin_fmaf(D, xv[i], ys[i]);
+                    ((S *)a.dz)[o] = E::from(dyv[i] * yv * (sg * (1.0f + zv[i] * (1.0f - sg))));
+                }
+            }
+        }
+        __syncthreads();
+        if (tid < TS * N4) {
+            const int n = tid % N4;
+            const long long tt = t + tid / N4;
+            if (n < a.n && tt < k.t1) {
+                const long long o = ((long long)c.block * a.q.tokens + tt) * a.n + n;
+                a.part_B[o] = (sb[0][tid] + sb[1][tid]) + (sb[2][tid] + sb[3][tid]);
+                a.part_C[o] = (sc[0][tid] + sc[1][tid]) + (sc[2][tid] + sc[3][tid]);
+            }
+        }
+    }
+    // a slot that no chunk uses adds nothing
+    if (!c.valid) return;
+    write_nl<NL>(a.part_A + at * a.n, a.n, part, dA);
+    sum_D = quad_sum(sum_D);
+    sum_bias = quad_sum(sum_bias);
+    if (part == 0) {
+        a.part_D[at] = sum_D;
+        a.part_bias[at] = sum_bias;
+    }
+    if (!joined && a.dinitial && k.valid)
+        write_nl<NL>(a.dinitial + ((long long)k.s * a.d + c.ch) * a.n, a.n, part, carry);
+}
+
+// Adds the partial sums in ascending order.  Blocks: first dB and dC, a thread
+// to a value; then dA, dD and ddt_bias.
+template <class E>
+__global__ __launch_bounds__(256) void scan_sum_kernel(ScanArgs a, unsigned bc_blocks)
+{
+    using S = typename E::S;
+    if (blockIdx.x < bc_blocks) {
+        const long long i = (long long)blockIdx.x * 256 + threadIdx.x, per = a.q.tokens * a.n;
+        if (i >= per * a.groups) return;
+        const int n = (int)(i % a.n), grp = (int)(i / a.n % a.groups);
+        const long long t = i / ((long long)a.n * a.groups);
+        float b = 0.0f, c = 0.0f;
+        const long long o = (long long)grp * a.blocks_per_group * per + t * a.n + n;
+        for (int k = 0; k < a.blocks_per_group; ++k) {
+            b += a.part_B[o + k * per];
+            c += a.part_C[o + k * per];
+        }
+        ((S *)a.dB)[i] = E::from(b);
+        ((S *)a.dC)[i] = E::from(c);
+        return;
+    }
+    long long i = (long long)(blockIdx.x - bc_blocks) * 256 + threadIdx.x;
+    const long long dn = (long long)a.d * a.n;
+    const float *p;
+    float *out;
+    long long per = a.d;
+    if (i < dn) {
+        p = a.part_A;
+        out = a.dA;
+        per = dn;
+    } else if ((i -= dn) < a.d) {
+        p = a.part_D;
+        out = a.dD;
+    } else {
+        i -= a.d;
+        p = a.part_bias;
+        out = a.ddt_bias;
+    }
+    if (i >= per || !out) return;
+    float v = 0.0f;
+    for (int s = 0; s < a.slots; ++s) v += p[s * per + i];
+    out[i] = v;
+}
+
+}  // namespace
+
+hipError_t launch_scan_grad(int dtype, const ScanArgs &a, hipStream_t st)
+{
+    const dim3 grid((unsigned)a.slots, (unsigned)(a.blocks_per_group * a.groups));
+    return scan_by_type(dtype, a.n, [&](auto e, auto nl) {
+        using E = decltype(e);
+        constexpr int NL = decltype(nl)::value;
+        if (a.chunk_state) {
+            scan_keep_kernel<E, NL, true><<<grid, 256, 0, st>>>(a);
+            launch_scan_join(a, st);
+        } else {
+            scan_keep_kernel<E, NL, false><<<grid, 256, 0, st>>>(a);
+        }
+        scan_back_kernel<E, NL><<<grid, 256, 0, st>>>(a);
+        const unsigned bc = (unsigned)((a.q.tokens * a.groups * a.n + 255) / 256);
+        const unsigned rest = (unsigned)(((long long)a.d * (a.n + 2) + 255) / 256);
+        scan_sum_kernel<E><<<dim3(bc + rest), 256, 0, st>>>(a, bc);
+        return hipGetLastError();
+    });
+}
+
+}  // namespace cnv

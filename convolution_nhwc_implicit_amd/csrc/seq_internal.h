@@ -1,0 +1,88 @@
+// seq_internal.h -- kernel arguments and launchers of the sequence operators,
+// shared by the host side (seq_api.cpp) and the kernels.  Not part of the ABI.
+#pragma once
+
+#include "seq_common.h"
+
+namespace cnv {
+
+// ---- causal convolution (causal_conv.hip) -------------------------------------
+constexpr int kConvUnroll = 4;    // rows whose loads are issued together
+constexpr int kConvBytes = 16;    // bytes of channels per thread: forward,
+constexpr int kConvGradBytes = 8; // and gradients and step (more live values per channel)
+
+struct ConvArgs {
+    Seqs q;
+    int d, silu;
+    int lanes;       // threads of a block along channels (a power of two, at most 64)
+    int run;         // rows per thread
+    int run_blocks;  // blocks along y that walk rows; the rest handle states
+    RowStride xs, dys;
+    const void *x, *weight, *bias, *initial, *dy, *dfinal;
+    void *y;          // y, or dx in the gradient pass
+    void *final_state, *dinitial;
+    float *partial;   // [run_blocks][w+1][d]
+    void *dweight, *dbias;
+};
+
+struct ConvStepArgs {
+    int rows, pool, d, silu, lanes;
+    long long x_row;
+    const void *x, *weight, *bias;
+    const int *slots;
+    void *state, *y;
+};
+
+hipError_t launch_conv(int dtype, int w, const ConvArgs &a, dim3 grid, hipStream_t st);
+hipError_t launch_conv_grad(int dtype, int w, const ConvArgs &a, dim3 grid, hipStream_t st);
+hipError_t launch_conv_step(int dtype, int w, const ConvStepArgs &a, dim3 grid, hipStream_t st);
+
+// ---- selective scan (selective_scan.hip, selective_scan_grad.hip) ----------------
+constexpr int kScanChannels = 64;  // channels of a workgroup (16 to a wave)
+
+struct ScanArgs {
+    Seqs q;
+    int d, n, groups, softplus;
+    int blocks_per_group;  // workgroups along the channels of one group
+    int chunk;             // tokens per chunk, a multiple of 16
+    int chunks;            // chunks per sequence (dense)
+    int slots;             // chunks in all; for packed sequences an upper bound
+    RowStride xs, dts, bs, cs, zs, dys;
+    long long b_group, c_group;  // strides between groups of B and C
+    const void *x, *dt, *B, *C, *z, *dy;
+    const float *A, *D, *dt_bias, *initial, *dfinal;
+    void *y;               // y [tokens][d]
+    float *final_state, *dinitial;
+    // workspace: per chunk the state it ends with (from zero; then the state it starts
+    // with), the sum of its steps, and the like for the gradient
+    float *chunk_state;    // [slots][d][n]
+    float *chunk_delta;    // [slots][d]
+    float *chunk_back;     // [slots][d][n]
+    float *check;          // [tokens/TS + slots + 1][d][n]: states before each step of TS tokens
+    float *check_delta;    // [tokens/TS + slots + 1][d]: sums of steps before it
+    float *part_A;         // [slots][d][n]
+    float *part_D;         // [slots][d], and the same for dt_bias
+    float *part_bias;
+    float *part_B, *part_C; // [channel blocks][tokens][n]
+    void *du, *ddt, *dz, *dB, *dC;
+    float *dA, *dD, *ddt_bias;
+};
+
+struct ScanStepArgs {
+    int rows, pool, d, n, groups, softplus;
+    long long x_row, dt_row, b_row, c_row, z_row, b_group, c_group;
+    const void *x, *dt, *B, *C, *z;
+    const float *A, *D, *dt_bias;
+    const int *slots;
+    float *state;
+    void *y;
+};
+
+// tokens a wave takes at once: its states' decays and values stay in registers
+constexpr int scan_step_tokens(int n) { return n <= 16 ? 16 : n <= 32 ? 8 : 4; }
+
+hipError_t launch_scan(int dtype, const ScanArgs &a, hipStream_t st);
+hipError_t launch_scan_grad(int dtype, const ScanArgs &a, hipStream_t st);
+hipError_t launch_scan_step(int dtype, const ScanStepArgs &a, hipStream_t st);
+
+}  // namespace cnv
