@@ -12,6 +12,6 @@ from .binding import (  # noqa: F401
     load, problem_from, wgrad, workspace_for,
 )
 from .sequence import (  # noqa: F401
-    causal_conv, causal_conv_grad, causal_conv_step, selective_scan, selective_scan_grad,
-    selective_scan_step,
+    causal_conv, causal_conv_grad, causal_conv_step, fp8_matmul, fp8_quantize, selective_scan,
+    selective_scan_grad, selective_scan_step,
 )

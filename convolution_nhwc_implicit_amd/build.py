@@ -21,7 +21,8 @@ LIB = os.path.join(PKG, "libconv2d_nhwc.so")
 ARCH = "gfx950"
 
 SOURCES = ["api.cpp", "igemm.hip", "band.hip", "wino.hip", "wgrad.hip", "wgrad_band.hip", "direct.hip", "repack.hip", "fewchan.hip", "fewchan_wgrad.hip", "fewchan_dgrad.hip", "pointwise.hip", "pointwise_wgrad.hip", "patch.hip",
-           "seq_api.cpp", "causal_conv.hip", "selective_scan.hip", "selective_scan_grad.hip"]
+           "seq_api.cpp", "causal_conv.hip", "selective_scan.hip", "selective_scan_grad.hip",
+           "fp8_quantize.hip", "fp8_matmul.hip"]
 
 COMMON_FLAGS = [
     "-x", "hip", f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",

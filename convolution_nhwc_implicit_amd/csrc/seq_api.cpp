@@ -432,4 +432,75 @@ int selective_scan_step(const selective_scan_step_problem_t *p, int dtype, const
     return status(launch_scan_step(dtype, a, (hipStream_t)stream));
 }
 
+int fp8_quantize(int form, int dtype, int m, int k, const void *x, long long x_row, void *q, long long q_pitch,
+                 float *scale, void *stream)
+{
+    if (form != FP8_ROWS && form != FP8_TRANSPOSE && form != FP8_BLOCKS) return CONV2D_ERR_INVALID_ARGUMENT;
+    if (m < 0 || k < 0 || x_row < 0) return CONV2D_ERR_INVALID_ARGUMENT;
+    const long long len = form == FP8_TRANSPOSE ? m : k;
+    if (q_pitch < len || q_pitch > ceil_div(len, kFp8Block) * kFp8Block) return CONV2D_ERR_INVALID_ARGUMENT;
+    if (!float_type(dtype) || q_pitch % 16) return CONV2D_ERR_UNSUPPORTED;
+    if (m == 0 || k == 0) return CONV2D_OK;
+    if (!x || !q || !scale) return CONV2D_ERR_INVALID_ARGUMENT;
+    if (!aligned(x, bytes_of(dtype)) || !aligned(q, 16) || !aligned(scale, 4)) return CONV2D_ERR_UNSUPPORTED;
+    if (form == FP8_TRANSPOSE && ceil_div(k, 64) > kMaxGridY) return CONV2D_ERR_UNSUPPORTED;
+    if (form == FP8_BLOCKS && ceil_div(m, kFp8Block) > kMaxGridY) return CONV2D_ERR_UNSUPPORTED;
+    if (ceil_div(k, kFp8Block) * m > kMaxRows * 16) return CONV2D_ERR_UNSUPPORTED;
+    const Fp8QuantArgs a = {m, k, x_row, q_pitch, x, (uint8_t *)q, scale};
+    return status(launch_fp8_quantize(form, dtype, a, (hipStream_t)stream));
+}
+
+static int check_matmul(const fp8_matmul_problem_t *p, int dtype)
+{
+    if (!p || p->m < 0 || p->n < 0 || p->k < 0 || (p->b_blocks != 0 && p->b_blocks != 1) || p->a_pitch < p->k ||
+        p->b_pitch < p->k)
+        return CONV2D_ERR_INVALID_ARGUMENT;
+    if (!float_type(dtype) || p->a_pitch % 16 || p->b_pitch % 16) return CONV2D_ERR_UNSUPPORTED;
+    // a tile's rows are read through 32-bit offsets
+    if (p->a_pitch > (1LL << 22) || p->b_pitch > (1LL << 22)) return CONV2D_ERR_UNSUPPORTED;
+    return CONV2D_OK;
+}
+
+int fp8_matmul_workspace_size(const fp8_matmul_problem_t *prob, int dtype, size_t *bytes)
+{
+    const int r = check_matmul(prob, dtype);
+    if (r != CONV2D_OK) return r;
+    if (!bytes) return CONV2D_ERR_INVALID_ARGUMENT;
+    *bytes = 0;
+    if (prob->m > 0 && prob->n > 0)
+        *bytes = fp8_matmul_bytes(prob->m, prob->n, fp8_matmul_plan(prob->m, prob->n, (int)ceil_div(prob->k, kFp8Block)));
+    return CONV2D_OK;
+}
+
+int fp8_matmul(const fp8_matmul_problem_t *prob, int dtype, const void *a, const float *a_scale,
+               const void *b, const float *b_scale, void *out, void *workspace, size_t workspace_bytes,
+               void *stream)
+{
+    const int r = check_matmul(prob, dtype);
+    if (r != CONV2D_OK) return r;
+    if (prob->m == 0 || prob->n == 0) return CONV2D_OK;
+    if (!out || (prob->k > 0 && (!a || !a_scale || !b || !b_scale))) return CONV2D_ERR_INVALID_ARGUMENT;
+    if (!aligned(a, 16) || !aligned(b, 16) || !all_aligned(4, {a_scale, b_scale}) || !aligned(out, bytes_of(dtype)) ||
+        !aligned(workspace, 16))
+        return CONV2D_ERR_UNSUPPORTED;
+    const Fp8Plan plan = fp8_matmul_plan(prob->m, prob->n, (int)ceil_div(prob->k, kFp8Block));
+    const size_t need = fp8_matmul_bytes(prob->m, prob->n, plan);
+    if (need && !workspace) return CONV2D_ERR_INVALID_ARGUMENT;
+    if (workspace_bytes < need) return CONV2D_ERR_WORKSPACE_TOO_SMALL;
+    Fp8MatmulArgs m = {};
+    m.m = prob->m;
+    m.n = prob->n;
+    m.k = prob->k;
+    m.kb = (int)ceil_div(prob->k, kFp8Block);
+    m.b_blocks = prob->b_blocks;
+    m.a_pitch = prob->a_pitch;
+    m.b_pitch = prob->b_pitch;
+    m.a = (const uint8_t *)a;
+    m.b = (const uint8_t *)b;
+    m.a_scale = a_scale;
+    m.b_scale = b_scale;
+    m.out = out;
+    return status(launch_fp8_matmul(dtype, m, plan, workspace, (hipStream_t)stream));
+}
+
 }  // extern "C"

@@ -85,4 +85,35 @@ hipError_t launch_scan(int dtype, const ScanArgs &a, hipStream_t st);
 hipError_t launch_scan_grad(int dtype, const ScanArgs &a, hipStream_t st);
 hipError_t launch_scan_step(int dtype, const ScanStepArgs &a, hipStream_t st);
 
+// ---- fp8 products (fp8_quantize.hip, fp8_matmul.hip) -------------------------------
+constexpr int kFp8Block = 128;  // values along the summed axis that share a scale
+
+struct Fp8QuantArgs {
+    int m, k;
+    long long x_row, q_pitch;
+    const void *x;
+    uint8_t *q;
+    float *scale;
+};
+
+struct Fp8MatmulArgs {
+    int m, n, k, kb;  // kb: blocks along k
+    int b_blocks;
+    long long a_pitch, b_pitch;
+    const uint8_t *a, *b;
+    const float *a_scale, *b_scale;
+    void *out;
+    int tiles_m, tiles_n;
+    int kb_split;  // blocks along k per workgroup
+};
+
+struct Fp8Plan {
+    int shape, splits, per;  // tile shape; workgroups along k, and blocks of each
+};
+
+hipError_t launch_fp8_quantize(int form, int dtype, const Fp8QuantArgs &a, hipStream_t st);
+Fp8Plan fp8_matmul_plan(int m, int n, int kb);
+size_t fp8_matmul_bytes(int m, int n, const Fp8Plan &p);
+hipError_t launch_fp8_matmul(int dtype, const Fp8MatmulArgs &a, const Fp8Plan &p, void *workspace, hipStream_t st);
+
 }  // namespace cnv

@@ -58,6 +58,13 @@ class SelectiveScanStepProblem(ctypes.Structure):
                 [(f, _ll) for f in ("x_row", "dt_row", "b_row", "c_row", "z_row", "b_group", "c_group")])
 
 
+class Fp8MatmulProblem(ctypes.Structure):
+    _fields_ = [(f, _i) for f in ("m", "n", "k", "b_blocks")] + [("a_pitch", _ll), ("b_pitch", _ll)]
+
+
+FP8_ROWS, FP8_TRANSPOSE, FP8_BLOCKS = 0, 1, 2
+FP8_BLOCK = 128  # values along the summed axis that share a scale
+
 _P = ctypes.POINTER
 _SIGNATURES = {
     "causal_conv": [_P(CausalConvProblem), _i] + [_vp] * 7,
@@ -69,6 +76,9 @@ _SIGNATURES = {
     "selective_scan_grad_workspace_size": [_P(SelectiveScanProblem), _i, _P(_sz)],
     "selective_scan_grad": [_P(SelectiveScanProblem), _i] + [_vp] * 11 + [_P(SelectiveScanGrads), _vp, _sz, _vp],
     "selective_scan_step": [_P(SelectiveScanStepProblem), _i] + [_vp] * 12,
+    "fp8_quantize": [_i, _i, _i, _i, _vp, _ll, _vp, _ll, _vp, _vp],
+    "fp8_matmul_workspace_size": [_P(Fp8MatmulProblem), _i, _P(_sz)],
+    "fp8_matmul": [_P(Fp8MatmulProblem), _i] + [_vp] * 6 + [_sz, _vp],
 }
 _lib = None
 
@@ -368,3 +378,69 @@ def selective_scan_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, sof
                                           C.data_ptr(), _ptr(D), _ptr(z), _ptr(dt_bias), sp_state, sp,
                                           y.data_ptr(), stream), "selective_scan_step")
     return y
+
+
+# ------------------------------------------------------------ block-scaled fp8 products
+
+def _blocks(v):
+    return -(-v // FP8_BLOCK)
+
+
+def fp8_quantize(x, transpose=False, blocks=False):
+    """x [m][k] to e4m3 with a scale for every 128 values of a row: (q [m][k], scale [m][ceil(k/128)]).
+
+    transpose: of x's transpose, q [k][m] and scale [k][ceil(m/128)].  blocks: a scale for every 128 x 128
+    values (weights), scale [ceil(m/128)][ceil(k/128)].  Scales are the least powers of two (at least 2^-126)
+    that bring a block's finite values into e4m3's range; infinities and NaN become NaN.  q's rows are padded
+    with zeros to a multiple of 16 bytes; q is a view of them."""
+    code = _float(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be [m][k]")
+    if transpose and blocks:
+        raise ValueError("blocks of 128 x 128 are quantised as they lie")
+    _tensor(x, "x", x.dtype, None)
+    (m, k), dev = x.shape, x.device
+    rows, cols = (k, m) if transpose else (m, k)
+    pitch = -(-cols // 16) * 16
+    form = FP8_TRANSPOSE if transpose else FP8_BLOCKS if blocks else FP8_ROWS
+    with _On(dev) as stream:
+        q = torch.empty((rows, pitch), dtype=torch.float8_e4m3fn, device=dev)
+        scale = torch.empty((_blocks(rows) if blocks else rows, _blocks(cols)), dtype=torch.float32, device=dev)
+        _raise(load().fp8_quantize(form, code, m, k, x.data_ptr(), _row_stride(x), q.data_ptr(), pitch,
+                                   scale.data_ptr(), stream), "fp8_quantize")
+    return (q if pitch == cols else q[:, :cols]), scale
+
+
+def _fp8_operand(q, scale, name, rows):
+    _tensor(q, name, torch.float8_e4m3fn, None)
+    if q.dim() != 2:
+        raise ValueError(f"{name} must be a matrix")
+    kb = _blocks(q.shape[1])
+    blocks = rows == "blocks" and q.shape[0] != 1 and scale.shape[0] != q.shape[0]
+    _dense(scale, f"{name}_scale", torch.float32, (_blocks(q.shape[0]) if blocks else q.shape[0], kb), q.device)
+    pitch = q.stride(0) if q.shape[0] > 1 and q.shape[1] > 0 else -(-q.shape[1] // 16) * 16
+    if pitch % 16 or pitch < q.shape[1]:
+        raise ValueError(f"{name}'s rows must start on 16-byte steps (fp8_quantize lays them out so)")
+    return pitch, blocks
+
+
+def fp8_matmul(a, a_scale, b, b_scale, out_dtype=torch.bfloat16):
+    """a times b's transpose: out [m][n] in out_dtype (float16, bfloat16 or float32) of e4m3 operands a [m][k]
+    and b [n][k] with float32 scales of 128 values along k: a_scale [m][ceil(k/128)], and b_scale
+    [n][ceil(k/128)] or [ceil(n/128)][ceil(k/128)].  Scales may be any values; powers of two cost no time.
+    Sums are float32, rounded once."""
+    a_pitch, _ = _fp8_operand(a, a_scale, "a", "rows")
+    b_pitch, blocks = _fp8_operand(b, b_scale, "b", "blocks")
+    (m, k), n, dev = a.shape, b.shape[0], a.device
+    if b.shape[1] != k or b.device != dev:
+        raise ValueError(f"b must be [n][{k}] on {dev}, got {tuple(b.shape)} on {b.device}")
+    code = _CODE.get(out_dtype)
+    if code is None:
+        raise TypeError(f"out_dtype must be float16, bfloat16 or float32, got {out_dtype}")
+    prob = Fp8MatmulProblem(m, n, k, int(blocks), a_pitch, b_pitch)
+    with _On(dev) as stream:
+        out = torch.empty((m, n), dtype=out_dtype, device=dev)
+        ws, need = _workspace("fp8_matmul_workspace_size", prob, code, dev)
+        _raise(load().fp8_matmul(prob, code, a.data_ptr(), a_scale.data_ptr(), b.data_ptr(), b_scale.data_ptr(),
+                                 out.data_ptr(), _ptr(ws), need, stream), "fp8_matmul")
+    return out

@@ -176,6 +176,51 @@ int selective_scan_step(const selective_scan_step_problem_t *prob, int dtype, co
                         const float *A, const void *B, const void *C, const float *D, const void *z,
                         const float *dt_bias, float *state, const int *slots, void *y, void *stream);
 
+/*
+ * Block-scaled fp8 products.  An fp8 operand is a matrix of e4m3 bytes (OCP
+ * e4m3fn: 448 is the largest, no infinities) with an fp32 scale for every 128
+ * values along the summed axis: of one row each, or (weights) of 128 rows
+ * together.  Value [r][k] stands for q[r][k] * scale[r or r / 128][k / 128].
+ *
+ * fp8_quantize: x [m][k] (dtype, row stride x_row, in elements) to such an
+ * operand.  The scale is the least power of two, at least 2^-126, that brings
+ * the finite values of its block into e4m3's range, so that it costs no
+ * accuracy; infinities and NaN become NaN and leave the others as they are.
+ *   FP8_ROWS       q [m][q_pitch], scale [m][ceil(k/128)]
+ *   FP8_TRANSPOSE  the operand is x's transpose: q [k][q_pitch], scale [k][ceil(m/128)]
+ *   FP8_BLOCKS     q [m][q_pitch], scale [ceil(m/128)][ceil(k/128)]
+ * q_pitch is a multiple of 16 and at least the operand's row length, less than
+ * its whole blocks of 128 more; q is 16-byte aligned.  Bytes past a row's end
+ * are set to zero.
+ */
+#define FP8_ROWS 0
+#define FP8_TRANSPOSE 1
+#define FP8_BLOCKS 2
+int fp8_quantize(int form, int dtype, int m, int k, const void *x, long long x_row, void *q,
+                 long long q_pitch, float *scale, void *stream);
+
+/*
+ * out[i][j] = sum_k a[i][k] a_scale[i][k/128] * b[j][k] b_scale[j or j/128][k/128],
+ * summed in fp32, rounded once to dtype (CONV2D_DTYPE_F16, _BF16 or _F32).
+ *   a [m][k] with pitch a_pitch, a_scale [m][ceil(k/128)]
+ *   b [n][k] with pitch b_pitch, b_scale [n][ceil(k/128)], or with b_blocks = 1
+ *     [ceil(n/128)][ceil(k/128)]; scales are any fp32 values
+ *   out [m][n] dense; must not overlap the operands
+ * a and b are 16-byte aligned, their pitches multiples of 16; bytes past a row's
+ * end are read but have no influence.  The workspace (fp8_matmul_workspace_size;
+ * 16-byte aligned; the size may be 0) holds partial sums over k.
+ */
+typedef struct fp8_matmul_problem {
+    int m, n, k;
+    int b_blocks; /* 0 or 1 */
+    long long a_pitch, b_pitch;
+} fp8_matmul_problem_t;
+
+int fp8_matmul_workspace_size(const fp8_matmul_problem_t *prob, int dtype, size_t *bytes);
+int fp8_matmul(const fp8_matmul_problem_t *prob, int dtype, const void *a, const float *a_scale,
+               const void *b, const float *b_scale, void *out, void *workspace, size_t workspace_bytes,
+               void *stream);
+
 #ifdef __cplusplus
 }
 #endif
