@@ -80,11 +80,14 @@ __device__ inline float softplus_f32(float raw)
     return raw != raw ? raw : r;  // the maximum above drops a NaN
 }
 
+// A value that every lane of the wave holds, in a scalar register.
+__device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
 // The chunk that a workgroup walks.
 struct Chunk {
     int s;            // sequence
     bool first, last; // of its sequence
-    long long t0, t1; // its rows
+    int t0, t1;       // its rows
     bool valid;
 };
 
@@ -101,15 +104,16 @@ __device__ inline Chunk find_chunk(const ScanArgs &a, int slot)
 {
     Chunk r;
     int c = 0, count = a.chunks;
-    r.valid = true;
+    bool found = true;
+    r.s = 0;
     if (!a.q.start) {
         r.s = slot / a.chunks;
         c = slot % a.chunks;
     } else {
         const int lane = threadIdx.x % 64;
         int base = 0;
-        r.valid = false;
-        for (int s0 = 0; s0 < a.q.seqs && !r.valid; s0 += 64) {
+        found = false;
+        for (int s0 = 0; s0 < a.q.seqs && !found; s0 += 64) {
             const int mine = s0 + lane < a.q.seqs ? chunks_of(a, s0 + lane) : 0;
             int incl = mine;
             for (int o = 1; o < 64; o <<= 1) {
@@ -122,21 +126,23 @@ __device__ inline Chunk find_chunk(const ScanArgs &a, int slot)
                 r.s = s0 + at;
                 count = __shfl(mine, at);
                 c = slot - (base + __shfl(incl, at) - count);
-                r.valid = true;
+                found = true;
             }
             base += __shfl(incl, 63);
         }
-        if (!r.valid) return r;
-        r.s = __builtin_amdgcn_readfirstlane(r.s);
-        c = __builtin_amdgcn_readfirstlane(c);
-        count = __builtin_amdgcn_readfirstlane(count);
     }
+    r.s = uniform(r.s);
+    c = uniform(c);
+    count = uniform(count);
+    r.valid = found;
     r.first = c == 0;
     r.last = c == count - 1;
     const long long b = a.q.begin(r.s), e = a.q.end(r.s);
-    r.t0 = b + (long long)c * a.chunk;
-    r.t1 = r.t0 + a.chunk < e ? r.t0 + a.chunk : e;
-    if (r.t1 < r.t0) r.t1 = r.t0;
+    long long t0 = b + (long long)c * a.chunk;
+    if (t0 > e) t0 = e;
+    const long long t1 = t0 + a.chunk < e ? t0 + a.chunk : e;
+    r.t0 = uniform((int)t0);
+    r.t1 = found ? uniform((int)t1) : r.t0;
     return r;
 }
 
@@ -144,9 +150,82 @@ __device__ inline Chunk find_chunk(const ScanArgs &a, int slot)
 // chunks' ranges do not meet: each has one entry more than the whole steps
 // between its first row and the next chunk's.  Never past tokens/TS + slots.
 template <int TS>
-__device__ inline long long scan_keep_index(const Chunk &k, int slot, long long t)
+__device__ inline long long scan_keep_index(const Chunk &k, int slot, int t)
 {
     return k.t0 / TS + slot + (t - k.t0) / TS;
+}
+
+// ---- buffers -----------------------------------------------------------------
+// Tensors are read and written through buffer descriptors whose range ends with
+// the rows of the step at hand: what lies past it (rows after the chunk, lanes
+// without a channel or a state) reads as zero and is not written, without
+// branches, and a lane needs one 32-bit offset per tensor.
+constexpr uint32_t kNowhere = 0x80000000u;  // past every range
+
+__device__ inline __amdgpu_buffer_rsrc_t buffer_of(const void *p, uint32_t bytes)
+{
+    const uint64_t v = (uint64_t)p;
+    const uint64_t u = (uint64_t)(uint32_t)uniform((int)(uint32_t)v) | (uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32;
+    return __builtin_amdgcn_make_buffer_rsrc((void *)u, 0, uniform((int)bytes), 0x00020000);
+}
+// `rows` (at least 1) rows of `width` elements from element `at` of a tensor on
+template <class E>
+__device__ inline __amdgpu_buffer_rsrc_t rows_of(const void *p, long long at, int rows, long long row, int width)
+{
+    return buffer_of((const char *)p + at * E::kBytes, ((uint32_t)(rows - 1) * (uint32_t)row + (uint32_t)width) * E::kBytes);
+}
+template <class E>
+__device__ inline typename E::S get(__amdgpu_buffer_rsrc_t r, uint32_t off)
+{
+    if constexpr (E::kBytes == 2) return (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0);
+    else return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
+}
+template <class E>
+__device__ inline void put(__amdgpu_buffer_rsrc_t r, uint32_t off, float v)
+{
+    if constexpr (E::kBytes == 2) __builtin_amdgcn_raw_buffer_store_b16(E::from(v), r, off, 0, 0);
+    else __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), r, off, 0, 0);
+}
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+// NL neighbouring fp32 at a byte offset (a multiple of 4).
+template <int NL>
+__device__ inline void get_run(__amdgpu_buffer_rsrc_t r, uint32_t off, float (&v)[NL])
+{
+    if constexpr (NL == 1) {
+        v[0] = get<SF32>(r, off);
+    } else if constexpr (NL == 2) {
+        const u32x2 w = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0));
+        const uint32_t x = w[0], y = w[1];
+        v[0] = __builtin_bit_cast(float, x);
+        v[1] = __builtin_bit_cast(float, y);
+    } else {
+#pragma unroll
+        for (int j = 0; j < NL; j += 4) {
+            const f32x4 w = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off + 4 * j, 0, 0));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[j + e] = w[e];
+        }
+    }
+}
+template <int NL>
+__device__ inline void put_run(__amdgpu_buffer_rsrc_t r, uint32_t off, const float (&v)[NL])
+{
+    if constexpr (NL == 1) {
+        put<SF32>(r, off, v[0]);
+    } else if constexpr (NL == 2) {
+        u32x2 w;
+        w[0] = __builtin_bit_cast(uint32_t, v[0]);
+        w[1] = __builtin_bit_cast(uint32_t, v[1]);
+        __builtin_amdgcn_raw_buffer_store_b64(w, r, off, 0, 0);
+    } else {
+#pragma unroll
+        for (int j = 0; j < NL; j += 4) {
+            const f32x4 w = {v[j], v[j + 1], v[j + 2], v[j + 3]};
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, w), r, off + 4 * j, 0, 0);
+        }
+    }
 }
 
 // The channels of a workgroup and a lane.
@@ -167,58 +246,96 @@ struct Channels {
     }
 };
 
-// A lane's values of one step of TS tokens: token 4*i + part for i < TS/4.
-// Rows past the chunk are read from its last row and given no weight by the
-// caller.  base: the tensor's row t of the step, lane offset included.
-template <int TS>
-struct Rows {
-    uint32_t off[TS / 4];
-    __device__ inline void set(long long row, int ch, int part, long long rem)
+// A lane's place in a tensor of rows: token `part` of a step, its channel.
+// Token 4*i + part lies i * four rows further.
+template <class E>
+struct TokenAt {
+    uint32_t off, four;
+    __device__ inline TokenAt(const Channels &c, long long row)
+        : off(c.valid ? ((uint32_t)c.part * (uint32_t)row + (uint32_t)c.ch) * E::kBytes : kNowhere),
+          four(4 * (uint32_t)row * E::kBytes)
     {
+    }
+    __device__ inline uint32_t operator[](int i) const { return off + i * four; }
+};
+
+// A lane's NL states in an array [..][d][n] of fp32: those of one entry.
+template <int NL>
+struct StateAt {
+    uint32_t off;
+    int n, part, d;
+    __device__ inline StateAt(const ScanArgs &a, const Channels &c)
+        : off(c.valid ? ((uint32_t)c.ch * (uint32_t)a.n + (uint32_t)c.part * NL) * 4 : kNowhere), n(a.n), part(c.part), d(a.d)
+    {
+    }
+    __device__ inline __amdgpu_buffer_rsrc_t entry(const float *p, long long i) const
+    {
+        return buffer_of(p + i * d * n, (uint32_t)d * (uint32_t)n * 4);
+    }
+    __device__ inline void load(const float *p, long long i, float (&v)[NL]) const
+    {
+        const __amdgpu_buffer_rsrc_t r = entry(p, i);
+        if (n == 4 * NL) {
+            get_run<NL>(r, off, v);
+        } else {
 #pragma unroll
-        for (int i = 0; i < TS / 4; ++i) {
-            const int t = 4 * i + part;
-            const uint32_t r = (uint32_t)(t < rem ? t : (int)rem - 1);
-            off[i] = r * (uint32_t)row + (uint32_t)ch;
+            for (int j = 0; j < NL; ++j) v[j] = get<SF32>(r, part * NL + j < n ? off + 4 * j : kNowhere);
+        }
+    }
+    __device__ inline void store(float *p, long long i, const float (&v)[NL]) const
+    {
+        const __amdgpu_buffer_rsrc_t r = entry(p, i);
+        if (n == 4 * NL) {
+            put_run<NL>(r, off, v);
+        } else {
+#pragma unroll
+            for (int j = 0; j < NL; ++j) put<SF32>(r, part * NL + j < n ? off + 4 * j : kNowhere, v[j]);
         }
     }
 };
+
+// A value per channel in an array [..][d], of entry i, read by every lane of
+// the channel or written by its first.
+__device__ inline float channel_load(const float *p, long long i, const ScanArgs &a, const Channels &c)
+{
+    return get<SF32>(buffer_of(p + i * a.d, (uint32_t)a.d * 4), c.valid ? (uint32_t)c.ch * 4 : kNowhere);
+}
+__device__ inline void channel_store(float *p, long long i, const ScanArgs &a, const Channels &c, float v)
+{
+    put<SF32>(buffer_of(p + i * a.d, (uint32_t)a.d * 4), c.valid && c.part == 0 ? (uint32_t)c.ch * 4 : kNowhere, v);
+}
 
 // B and C of a step as fp32 in LDS, [TS][4*NL].  Thread i of the workgroup
 // takes value i (TS * 4*NL <= 256).
 template <class E, int NL, int TS>
 struct StageBC {
     static constexpr int kCount = TS * 4 * NL;
-    float b, c;
-    __device__ inline void load(const ScanArgs &a, const Chunk &k, int group, long long t, bool want_c)
+    static_assert(kCount <= 256, "a value per thread");
+    typename E::S b, c;
+    uint32_t boff, coff;
+    __device__ inline StageBC(const ScanArgs &a)
     {
-        b = c = 0.0f;
-        const int tid = threadIdx.x;
-        if (tid >= kCount) return;
-        const long long tt = t + tid / (4 * NL);
-        const int n = tid % (4 * NL);
-        if (n < a.n && tt < k.t1) {
-            b = E::to(((const typename E::S *)a.B)[a.bs.at(a.q, k.s, tt) + group * a.b_group + n]);
-            if (want_c) c = E::to(((const typename E::S *)a.C)[a.cs.at(a.q, k.s, tt) + group * a.c_group + n]);
-        }
+        const uint32_t tok = threadIdx.x / (4 * NL), n = threadIdx.x % (4 * NL);
+        const bool mine = threadIdx.x < kCount && (int)n < a.n;
+        boff = mine ? (tok * (uint32_t)a.bs.row + n) * E::kBytes : kNowhere;
+        coff = mine ? (tok * (uint32_t)a.cs.row + n) * E::kBytes : kNowhere;
+    }
+    __device__ inline void load(const ScanArgs &a, const Chunk &k, int group, int t, bool want_c)
+    {
+        const int rows = k.t1 - t < TS ? k.t1 - t : TS;
+        b = get<E>(rows_of<E>(a.B, a.bs.at(a.q, k.s, t) + group * a.b_group, rows, a.bs.row, a.n), boff);
+        if (want_c) c = get<E>(rows_of<E>(a.C, a.cs.at(a.q, k.s, t) + group * a.c_group, rows, a.cs.row, a.n), coff);
     }
     __device__ inline void store(float *lb, float *lc) const
     {
         if (threadIdx.x < kCount) {
-            lb[threadIdx.x] = b;
-            if (lc) lc[threadIdx.x] = c;
+            lb[threadIdx.x] = E::to(b);
+            if (lc) lc[threadIdx.x] = E::to(c);
         }
     }
 };
 
-template <int NL>
-__device__ inline void load_states(const float *p, float (&v)[NL])
-{
-#pragma unroll
-    for (int j = 0; j < NL; ++j) v[j] = p[j];
-}
-
-// NL states of a lane in an [..][d][n] array; n may be short of 4*NL.
+// NL states of a lane at p, [n] of one channel; n may be short of 4*NL.
 template <int NL>
 __device__ inline void read_nl(const float *p, int n, int part, float (&v)[NL])
 {

@@ -24,54 +24,49 @@ __global__ __launch_bounds__(256) void scan_kernel(ScanArgs a)
     const Chunk k = find_chunk(a, slot);
     if (!k.valid || (LOCAL && k.last)) return;
     const Channels c(a, blockIdx.y);
+    const StateAt<NL> at(a, c);
     const int part = c.part;
-    const bool odd = part & 1, high = part & 2;
+    const bool odd = part & 1, high = part & 2, gated = !LOCAL && a.z;
 
     float A2[NL], h[NL];
-    read_nl<NL>(a.A + (long long)c.ch * a.n, a.n, part, A2);
+    at.load(a.A, 0, A2);
 #pragma unroll
     for (int j = 0; j < NL; ++j) {
         A2[j] *= kLog2e;
         h[j] = 0.0f;
     }
     if (!LOCAL) {
-        if (a.chunk_state) read_nl<NL>(a.chunk_state + ((long long)slot * a.d + c.ch) * a.n, a.n, part, h);
-        else if (a.initial) read_nl<NL>(a.initial + ((long long)k.s * a.d + c.ch) * a.n, a.n, part, h);
+        if (a.chunk_state) at.load(a.chunk_state, slot, h);
+        else if (a.initial) at.load(a.initial, k.s, h);
     }
-    const float bias = a.dt_bias ? a.dt_bias[c.ch] : 0.0f, D = !LOCAL && a.D ? a.D[c.ch] : 0.0f;
+    const float bias = a.dt_bias ? channel_load(a.dt_bias, 0, a, c) : 0.0f;
+    const float D = !LOCAL && a.D ? channel_load(a.D, 0, a, c) : 0.0f;
     float sum_delta = 0.0f;
 
     __shared__ float lb[2][TS * 4 * NL], lc[2][TS * 4 * NL];
-    Rows<TS> rx, rdt, rz, ry;
+    const TokenAt<E> ax(c, a.xs.row), adt(c, a.dts.row), az(c, gated ? a.zs.row : 0), ay(c, a.d);
     S x[G], dt[G], z[G];
-    StageBC<E, NL, TS> bc;
-    auto offsets = [&](long long rem) {
-        rx.set(a.xs.row, c.ch, part, rem);
-        rdt.set(a.dts.row, c.ch, part, rem);
-        if (!LOCAL) ry.set(a.d, c.ch, part, rem);
-        if (!LOCAL && a.z) rz.set(a.zs.row, c.ch, part, rem);
-    };
-    auto fetch = [&](long long t) {
-        const S *px = (const S *)a.x + a.xs.at(a.q, k.s, t), *pdt = (const S *)a.dt + a.dts.at(a.q, k.s, t);
+    StageBC<E, NL, TS> bc(a);
+    auto fetch = [&](int t) {
+        const int rows = k.t1 - t < TS ? k.t1 - t : TS;
+        const auto bx = rows_of<E>(a.x, a.xs.at(a.q, k.s, t), rows, a.xs.row, a.d);
+        const auto bdt = rows_of<E>(a.dt, a.dts.at(a.q, k.s, t), rows, a.dts.row, a.d);
 #pragma unroll
         for (int i = 0; i < G; ++i) {
-            x[i] = px[rx.off[i]];
-            dt[i] = pdt[rdt.off[i]];
+            x[i] = get<E>(bx, ax[i]);
+            dt[i] = get<E>(bdt, adt[i]);
         }
-        if (!LOCAL && a.z) {
-            const S *pz = (const S *)a.z + a.zs.at(a.q, k.s, t);
+        if (gated) {
+            const auto bz = rows_of<E>(a.z, a.zs.at(a.q, k.s, t), rows, a.zs.row, a.d);
 #pragma unroll
-            for (int i = 0; i < G; ++i) z[i] = pz[rz.off[i]];
+            for (int i = 0; i < G; ++i) z[i] = get<E>(bz, az[i]);
         }
         bc.load(a, k, c.group, t, !LOCAL);
     };
-    if (k.t0 < k.t1) {
-        offsets(k.t1 - k.t0);
-        fetch(k.t0);
-    }
+    if (k.t0 < k.t1) fetch(k.t0);
     int buf = 0;
-    for (long long t = k.t0; t < k.t1; t += TS, buf ^= 1) {
-        const long long rem = k.t1 - t;
+    for (int t = k.t0; t < k.t1; t += TS, buf ^= 1) {
+        const int rem = k.t1 - t;
         float delta[G], dx[G], xv[G], zv[G];
 #pragma unroll
         for (int i = 0; i < G; ++i) {
@@ -79,20 +74,15 @@ __global__ __launch_bounds__(256) void scan_kernel(ScanArgs a)
             const float raw = E::to(dt[i]) + bias;
             xv[i] = E::to(x[i]);
             delta[i] = a.softplus ? softplus_f32(raw) : raw;
-            dx[i] = valid ? delta[i] * xv[i] : 0.0f;
             delta[i] = valid ? delta[i] : 0.0f;  // a token that is not there leaves the state as it is
+            dx[i] = delta[i] * xv[i];
             if (LOCAL) sum_delta += delta[i];
-            if (!LOCAL) zv[i] = a.z ? E::to(z[i]) : 0.0f;
+            zv[i] = gated ? E::to(z[i]) : 0.0f;
         }
         bc.store(lb[buf], LOCAL ? nullptr : lc[buf]);
-        uint32_t yoff[G];
-#pragma unroll
-        for (int i = 0; i < G; ++i) yoff[i] = LOCAL ? 0 : ry.off[i];
-        if (rem > TS) {
-            if (rem < 2 * TS) offsets(rem - TS);
-            fetch(t + TS);
-        }
+        if (rem > TS) fetch(t + TS);
         __syncthreads();
+        const auto by = rows_of<E>(a.y, (long long)t * a.d, rem < TS ? rem : TS, a.d, a.d);
 #pragma unroll
         for (int i = 0; i < G; ++i) {
             float acc[4];
@@ -114,18 +104,16 @@ __global__ __launch_bounds__(256) void scan_kernel(ScanArgs a)
             token(std::integral_constant<int, 3>{});
             if (!LOCAL) {
                 float v = __builtin_fmaf(D, xv[i], quad_scatter_sum(acc[0], acc[1], acc[2], acc[3], odd, high));
-                if (a.z) v *= zv[i] * sigmoid_f32(zv[i]);
-                if (c.valid && 4 * i + part < rem) ((S *)a.y + t * a.d)[yoff[i]] = E::from(v);
+                if (gated) v *= zv[i] * sigmoid_f32(zv[i]);
+                put<E>(by, ay[i], v);
             }
         }
     }
     if (LOCAL) {
-        if (!c.valid) return;
-        write_nl<NL>(a.chunk_state + ((long long)slot * a.d + c.ch) * a.n, a.n, part, h);
-        sum_delta = quad_sum(sum_delta);
-        if (part == 0) a.chunk_delta[(long long)slot * a.d + c.ch] = sum_delta;
-    } else if (a.final_state && k.last && c.valid) {
-        write_nl<NL>(a.final_state + ((long long)k.s * a.d + c.ch) * a.n, a.n, part, h);
+        at.store(a.chunk_state, slot, h);
+        channel_store(a.chunk_delta, slot, a, c, quad_sum(sum_delta));
+    } else if (a.final_state && k.last) {
+        at.store(a.final_state, k.s, h);
     }
 }
 

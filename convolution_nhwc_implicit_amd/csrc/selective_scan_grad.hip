@@ -29,88 +29,79 @@ void launch_scan_join(const ScanArgs &a, hipStream_t st);
 namespace {
 
 // What a step's tokens read, as stored.
-template <class E, int G>
+template <class E, int TS>
 struct Tokens {
+    static constexpr int G = TS / 4;
     typename E::S x[G], dt[G], z[G], dy[G];
-};
-
-template <int TS>
-struct TokenRows {
-    Rows<TS> x, dt, z, dy;
-    __device__ inline void set(const ScanArgs &a, int ch, int part, long long rem)
+    TokenAt<E> ax, adt, az, ady;
+    __device__ inline Tokens(const ScanArgs &a, const Channels &c)
+        : ax(c, a.xs.row), adt(c, a.dts.row), az(c, a.z ? a.zs.row : 0), ady(c, a.dys.row)
     {
-        x.set(a.xs.row, ch, part, rem);
-        dt.set(a.dts.row, ch, part, rem);
-        if (a.z) z.set(a.zs.row, ch, part, rem);
-        dy.set(a.dys.row, ch, part, rem);
+    }
+    __device__ inline void fetch(const ScanArgs &a, const Chunk &k, int t, bool grad)
+    {
+        const int rows = k.t1 - t < TS ? k.t1 - t : TS;
+        const auto bx = rows_of<E>(a.x, a.xs.at(a.q, k.s, t), rows, a.xs.row, a.d);
+        const auto bdt = rows_of<E>(a.dt, a.dts.at(a.q, k.s, t), rows, a.dts.row, a.d);
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+            x[i] = get<E>(bx, ax[i]);
+            dt[i] = get<E>(bdt, adt[i]);
+        }
+        if (!grad) return;
+        const auto bdy = rows_of<E>(a.dy, a.dys.at(a.q, k.s, t), rows, a.dys.row, a.d);
+#pragma unroll
+        for (int i = 0; i < G; ++i) dy[i] = get<E>(bdy, ady[i]);
+        if (!a.z) return;
+        const auto bz = rows_of<E>(a.z, a.zs.at(a.q, k.s, t), rows, a.zs.row, a.d);
+#pragma unroll
+        for (int i = 0; i < G; ++i) z[i] = get<E>(bz, az[i]);
     }
 };
-
-template <class E, int TS, bool GRAD>
-__device__ inline void fetch_tokens(const ScanArgs &a, const Chunk &k, long long t, const TokenRows<TS> &r, Tokens<E, TS / 4> &o)
-{
-    using S = typename E::S;
-    const S *px = (const S *)a.x + a.xs.at(a.q, k.s, t), *pdt = (const S *)a.dt + a.dts.at(a.q, k.s, t);
-#pragma unroll
-    for (int i = 0; i < TS / 4; ++i) {
-        o.x[i] = px[r.x.off[i]];
-        o.dt[i] = pdt[r.dt.off[i]];
-    }
-    if (!GRAD) return;
-    const S *pdy = (const S *)a.dy + a.dys.at(a.q, k.s, t);
-#pragma unroll
-    for (int i = 0; i < TS / 4; ++i) o.dy[i] = pdy[r.dy.off[i]];
-    if (a.z) {
-        const S *pz = (const S *)a.z + a.zs.at(a.q, k.s, t);
-#pragma unroll
-        for (int i = 0; i < TS / 4; ++i) o.z[i] = pz[r.z.off[i]];
-    }
-}
 
 template <class E, int NL, bool CARRY>
 __global__ __launch_bounds__(256) void scan_keep_kernel(ScanArgs a)
 {
-    constexpr int TS = scan_step_tokens(4 * NL), G = TS / 4;
+    constexpr int TS = scan_grad_step_tokens(4 * NL), G = TS / 4;
     const int slot = blockIdx.x;
     const Chunk k = find_chunk(a, slot);
     if (!k.valid) return;
     const Channels c(a, blockIdx.y);
+    const StateAt<NL> at(a, c);
     const int part = c.part;
     float A2[NL], h[NL], P[NL], back[NL];
-    read_nl<NL>(a.A + (long long)c.ch * a.n, a.n, part, A2);
+    at.load(a.A, 0, A2);
 #pragma unroll
     for (int j = 0; j < NL; ++j) {
         A2[j] *= kLog2e;
         h[j] = back[j] = 0.0f;
         P[j] = 1.0f;
     }
-    if (!CARRY && a.initial && c.valid) read_nl<NL>(a.initial + ((long long)k.s * a.d + c.ch) * a.n, a.n, part, h);
-    const float bias = a.dt_bias ? a.dt_bias[c.ch] : 0.0f;
+    if (!CARRY && a.initial) at.load(a.initial, k.s, h);
+    const float bias = a.dt_bias ? channel_load(a.dt_bias, 0, a, c) : 0.0f;
     float sum_delta = 0.0f;
 
     __shared__ float lb[2][TS * 4 * NL], lc[2][TS * 4 * NL];
-    TokenRows<TS> rows;
-    Tokens<E, G> in;
-    StageBC<E, NL, TS> bc;
+    Tokens<E, TS> in(a, c);
+    StageBC<E, NL, TS> bc(a);
     if (k.t0 < k.t1) {
-        rows.set(a, c.ch, part, k.t1 - k.t0);
-        fetch_tokens<E, TS, CARRY>(a, k, k.t0, rows, in);
+        in.fetch(a, k, k.t0, CARRY);
         bc.load(a, k, c.group, k.t0, CARRY);
     }
     int buf = 0;
-    long long keep = scan_keep_index<TS>(k, slot, k.t0) * a.d + c.ch;
-    for (long long t = k.t0; t < k.t1; t += TS, buf ^= 1, keep += a.d) {
-        const long long rem = k.t1 - t;
+    for (int t = k.t0; t < k.t1; t += TS, buf ^= 1) {
+        const int rem = k.t1 - t;
+        const long long keep = scan_keep_index<TS>(k, slot, t);
         float delta[G], dx[G], g[G], step_delta = 0.0f;
-        if (c.valid) write_nl<NL>(a.check + keep * a.n, a.n, part, h);
-        if (CARRY && c.valid && part == 0) a.check_delta[keep] = sum_delta;
+        at.store(a.check, keep, h);
+        if (CARRY) channel_store(a.check_delta, keep, a, c, sum_delta);
 #pragma unroll
         for (int i = 0; i < G; ++i) {
             const bool valid = c.valid && 4 * i + part < rem;
             const float raw = E::to(in.dt[i]) + bias;
             delta[i] = a.softplus ? softplus_f32(raw) : raw;
-            dx[i] = valid ? delta[i] * E::to(in.x[i]) : 0.0f;
             delta[i] = valid ? delta[i] : 0.0f;
+            dx[i] = delta[i] * E::to(in.x[i]);
             step_delta += delta[i];
             g[i] = 0.0f;
             if (CARRY) {
@@ -119,14 +110,13 @@ __global__ __launch_bounds__(256) void scan_keep_kernel(ScanArgs a)
                     const float z = E::to(in.z[i]);
                     g[i] *= z * sigmoid_f32(z);
                 }
-                g[i] = valid ? g[i] : 0.0f;
+                g[i] = valid ? g[i] : 0.0f;  // an expanded tensor's rows (stride 0) all lie in range
             }
         }
         if (CARRY) sum_delta += quad_sum(step_delta);
         bc.store(lb[buf], CARRY ? lc[buf] : nullptr);
         if (rem > TS) {
-            if (rem < 2 * TS) rows.set(a, c.ch, part, rem - TS);
-            fetch_tokens<E, TS, CARRY>(a, k, t + TS, rows, in);
+            in.fetch(a, k, t + TS, CARRY);
             bc.load(a, k, c.group, t + TS, CARRY);
         }
         __syncthreads();
@@ -152,61 +142,59 @@ __global__ __launch_bounds__(256) void scan_keep_kernel(ScanArgs a)
             token(std::integral_constant<int, 3>{});
         }
     }
-    if (CARRY && c.valid) {
-        const long long at = (long long)slot * a.d + c.ch;
-        write_nl<NL>(a.chunk_state + at * a.n, a.n, part, h);
-        write_nl<NL>(a.chunk_back + at * a.n, a.n, part, back);
-        if (part == 0) a.chunk_delta[at] = sum_delta;
+    if (CARRY) {
+        at.store(a.chunk_state, slot, h);
+        at.store(a.chunk_back, slot, back);
+        channel_store(a.chunk_delta, slot, a, c, sum_delta);
     }
 }
 
 template <class E, int NL>
-__global__ __launch_bounds__(256, 2) void scan_back_kernel(ScanArgs a)
+__global__ __launch_bounds__(256, NL > 8 ? 1 : 2) void scan_back_kernel(ScanArgs a)
 {
-    constexpr int TS = scan_step_tokens(4 * NL), G = TS / 4, N4 = 4 * NL;
-    using S = typename E::S;
+    constexpr int TS = scan_grad_step_tokens(4 * NL), G = TS / 4, N4 = 4 * NL;
     const int slot = blockIdx.x, tid = threadIdx.x;
     const Chunk k = find_chunk(a, slot);
     const Channels c(a, blockIdx.y);
+    const StateAt<NL> at(a, c);
     const int part = c.part, row = tid % 64 / 16, wave = tid / 64;
     const bool odd = part & 1, high = part & 2;
-    const long long at = (long long)slot * a.d + c.ch;
     float A[NL], carry[NL], H0[NL], dA[NL], sum_D = 0.0f, sum_bias = 0.0f;
-    read_nl<NL>(a.A + (long long)c.ch * a.n, a.n, part, A);
+    at.load(a.A, 0, A);
 #pragma unroll
     for (int j = 0; j < NL; ++j) dA[j] = carry[j] = H0[j] = 0.0f;
     const bool joined = a.chunk_state != nullptr;
-    if (k.valid && c.valid) {
+    if (k.valid) {
         if (joined) {
-            read_nl<NL>(a.chunk_back + at * a.n, a.n, part, carry);
-            read_nl<NL>(a.chunk_state + at * a.n, a.n, part, H0);
+            at.load(a.chunk_back, slot, carry);
+            at.load(a.chunk_state, slot, H0);
         } else if (a.dfinal) {
-            read_nl<NL>(a.dfinal + ((long long)k.s * a.d + c.ch) * a.n, a.n, part, carry);
+            at.load(a.dfinal, k.s, carry);
         }
     }
-    const float bias = a.dt_bias ? a.dt_bias[c.ch] : 0.0f, D = a.D ? a.D[c.ch] : 0.0f;
+    const float bias = a.dt_bias ? channel_load(a.dt_bias, 0, a, c) : 0.0f;
+    const float D = a.D ? channel_load(a.D, 0, a, c) : 0.0f;
 
     __shared__ float lb[TS * N4], lc[TS * N4];
     __shared__ float sb[4][TS * N4], sc[4][TS * N4];  // the waves' sums of dB and dC
-    TokenRows<TS> rows;
-    Tokens<E, G> in;
-    StageBC<E, NL, TS> bc;
+    Tokens<E, TS> in(a, c);
+    StageBC<E, NL, TS> bc(a);
+    const TokenAt<E> ao(c, a.d);
+    // this thread's value of a step's dB and dC
+    const uint32_t sum_off = tid < TS * N4 && tid % N4 < a.n ? (uint32_t)(tid / N4 * a.n + tid % N4) * 4 : kNowhere;
     float kept[NL], kept_delta = 0.0f;
-    auto fetch = [&](long long t) {
-        fetch_tokens<E, TS, true>(a, k, t, rows, in);
+    auto fetch = [&](int t) {
+        in.fetch(a, k, t, true);
         bc.load(a, k, c.group, t, true);
-        const long long keep = scan_keep_index<TS>(k, slot, t) * a.d + c.ch;
-        read_nl<NL>(a.check + keep * a.n, a.n, part, kept);
-        if (joined) kept_delta = a.check_delta[keep];
+        const long long keep = scan_keep_index<TS>(k, slot, t);
+        at.load(a.check, keep, kept);
+        if (joined) kept_delta = channel_load(a.check_delta, keep, a, c);
     };
-    const long long len = k.valid ? k.t1 - k.t0 : 0;
-    long long t = k.t0 + (len - 1) / TS * TS;  // the last step, perhaps short
-    if (len > 0) {
-        rows.set(a, c.ch, part, k.t1 - t);
-        fetch(t);
-    }
-    for (long long left = (len + TS - 1) / TS; left > 0; --left, t -= TS) {
-        const long long rem = k.t1 - t < TS ? k.t1 - t : TS;
+    const int len = k.t1 - k.t0;
+    int t = k.t0 + (len - 1) / TS * TS;  // the last step, perhaps short
+    if (len > 0) fetch(t);
+    for (int left = (len + TS - 1) / TS; left > 0; --left, t -= TS) {
+        const int rem = k.t1 - t < TS ? k.t1 - t : TS;
         float delta[G], dx[G], xv[G], g[G], dyv[G], zv[G], sig_raw[G], h0[NL];
 #pragma unroll
         for (int i = 0; i < G; ++i) {
@@ -215,8 +203,9 @@ __global__ __launch_bounds__(256, 2) void scan_back_kernel(ScanArgs a)
             xv[i] = E::to(in.x[i]);
             delta[i] = a.softplus ? softplus_f32(raw) : raw;
             sig_raw[i] = a.softplus ? sigmoid_f32(raw) : 1.0f;
-            dx[i] = valid ? delta[i] * xv[i] : 0.0f;
+            sig_raw[i] = valid ? sig_raw[i] : 0.0f;  // so that ddt, whose sum is ddt_bias, is 0 where there is no token
             delta[i] = valid ? delta[i] : 0.0f;
+            dx[i] = delta[i] * xv[i];
             dyv[i] = E::to(in.dy[i]);
             zv[i] = a.z ? E::to(in.z[i]) : 0.0f;
             g[i] = a.z ? dyv[i] * (zv[i] * sigmoid_f32(zv[i])) : dyv[i];
@@ -224,14 +213,11 @@ __global__ __launch_bounds__(256, 2) void scan_back_kernel(ScanArgs a)
         }
 #pragma unroll
         for (int j = 0; j < NL; ++j) {
-            h0[j] = c.valid ? kept[j] : 0.0f;
+            h0[j] = kept[j];
             if (joined) h0[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(kept_delta * (A[j] * kLog2e)), H0[j], h0[j]);
         }
         bc.store(lb, lc);
-        if (left > 1) {
-            if (rem < TS) rows.set(a, c.ch, part, TS);
-            fetch(t - TS);
-        }
+        if (left > 1) fetch(t - TS);
         __syncthreads();
 
         float e[TS][NL], h[TS][NL], ys[G];
@@ -256,7 +242,10 @@ __global__ __launch_bounds__(256, 2) void scan_back_kernel(ScanArgs a)
             token(std::integral_constant<int, 2>{});
             token(std::integral_constant<int, 3>{});
             ys[i] = quad_scatter_sum(acc[0], acc[1], acc[2], acc[3], odd, high);
+            __builtin_amdgcn_sched_barrier(0);  // else every token's B and C are read ahead, and registers spill
         }
+        const auto bdu = rows_of<E>(a.du, (long long)t * a.d, rem, a.d, a.d);
+        const auto bddt = rows_of<E>(a.ddt, (long long)t * a.d, rem, a.d, a.d);
 #pragma unroll
         for (int i = G - 1; i >= 0; --i) {
             float inner[4], along[4], vb[NL][4], vc[NL][4];
@@ -281,6 +270,7 @@ __global__ __launch_bounds__(256, 2) void scan_back_kernel(ScanArgs a)
             token(std::integral_constant<int, 2>{});
             token(std::integral_constant<int, 1>{});
             token(std::integral_constant<int, 0>{});
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int j = 0; j < NL; ++j) {
                 const float tb = channel_sum4(vb[j][0], vb[j][1], vb[j][2], vb[j][3]);
@@ -292,42 +282,31 @@ __global__ __launch_bounds__(256, 2) void scan_back_kernel(ScanArgs a)
             }
             const float in_sum = quad_scatter_sum(inner[0], inner[1], inner[2], inner[3], odd, high);
             const float al_sum = quad_scatter_sum(along[0], along[1], along[2], along[3], odd, high);
-            const bool valid = c.valid && 4 * i + part < rem;
-            if (valid) {
-                const long long o = (t + 4 * i + part) * a.d + c.ch;
-                const float draw = __builtin_fmaf(xv[i], in_sum, al_sum) * sig_raw[i];
-                sum_D = __builtin_fmaf(g[i], xv[i], sum_D);
-                sum_bias += draw;
-                ((S *)a.du)[o] = E::from(__builtin_fmaf(delta[i], in_sum, D * g[i]));
-                ((S *)a.ddt)[o] = E::from(draw);
-                if (a.z) {
-                    const float sg = sigmoid_f32(zv[i]), yv = __builtin_fmaf(D, xv[i], ys[i]);
-                    ((S *)a.dz)[o] = E::from(dyv[i] * yv * (sg * (1.0f + zv[i] * (1.0f - sg))));
-                }
+            const float draw = __builtin_fmaf(xv[i], in_sum, al_sum) * sig_raw[i];
+            sum_D = __builtin_fmaf(g[i], xv[i], sum_D);
+            sum_bias += draw;
+            put<E>(bdu, ao[i], __builtin_fmaf(delta[i], in_sum, D * g[i]));
+            put<E>(bddt, ao[i], draw);
+            if (a.z) {
+                const float sg = sigmoid_f32(zv[i]), yv = __builtin_fmaf(D, xv[i], ys[i]);
+                put<E>(rows_of<E>(a.dz, (long long)t * a.d, rem, a.d, a.d), ao[i],
+                       dyv[i] * yv * (sg * (1.0f + zv[i] * (1.0f - sg))));
             }
         }
         __syncthreads();
         if (tid < TS * N4) {
-            const int n = tid % N4;
-            const long long tt = t + tid / N4;
-            if (n < a.n && tt < k.t1) {
-                const long long o = ((long long)c.block * a.q.tokens + tt) * a.n + n;
-                a.part_B[o] = (sb[0][tid] + sb[1][tid]) + (sb[2][tid] + sb[3][tid]);
-                a.part_C[o] = (sc[0][tid] + sc[1][tid]) + (sc[2][tid] + sc[3][tid]);
-            }
+            const long long o = ((long long)c.block * a.q.tokens + t) * a.n;
+            put<SF32>(buffer_of(a.part_B + o, (uint32_t)(rem * a.n) * 4), sum_off,
+                      (sb[0][tid] + sb[1][tid]) + (sb[2][tid] + sb[3][tid]));
+            put<SF32>(buffer_of(a.part_C + o, (uint32_t)(rem * a.n) * 4), sum_off,
+                      (sc[0][tid] + sc[1][tid]) + (sc[2][tid] + sc[3][tid]));
         }
     }
     // a slot that no chunk uses adds nothing
-    if (!c.valid) return;
-    write_nl<NL>(a.part_A + at * a.n, a.n, part, dA);
-    sum_D = quad_sum(sum_D);
-    sum_bias = quad_sum(sum_bias);
-    if (part == 0) {
-        a.part_D[at] = sum_D;
-        a.part_bias[at] = sum_bias;
-    }
-    if (!joined && a.dinitial && k.valid)
-        write_nl<NL>(a.dinitial + ((long long)k.s * a.d + c.ch) * a.n, a.n, part, carry);
+    at.store(a.part_A, slot, dA);
+    channel_store(a.part_D, slot, a, c, quad_sum(sum_D));
+    channel_store(a.part_bias, slot, a, c, quad_sum(sum_bias));
+    if (!joined && a.dinitial && k.valid) at.store(a.dinitial, k.s, carry);
 }
 
 // Adds the partial sums in ascending order.  Blocks: first dB and dC, a thread

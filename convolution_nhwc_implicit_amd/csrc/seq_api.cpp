@@ -11,7 +11,7 @@ using namespace cnv;
 namespace {
 
 constexpr long long kMaxRows = (1LL << 31) - 1;
-constexpr long long kMaxStride = (1LL << 26) - 1;
+constexpr long long kMaxStride = (1LL << 24) - 1;  // 16 rows of it in bytes fit 31 bits
 constexpr long long kMaxGridY = 65535;
 constexpr int kCUs = 256;  // MI355X
 
@@ -142,7 +142,7 @@ void scan_plan(const selective_scan_problem_t *p, long long want, bool grad, Sca
     s->delta = up(s->slots * d);
     s->check = s->check_delta = s->part_B = 0;
     if (grad) {
-        const long long steps = b.tokens / scan_step_tokens(p->n) + s->slots + 1;  // scan_keep_index
+        const long long steps = b.tokens / scan_grad_step_tokens(p->n) + s->slots + 1;  // scan_keep_index
         s->check = up(steps * dn);
         s->check_delta = up(steps * d);
         s->part_B = up((size_t)blocks * b.tokens * p->n * 4);

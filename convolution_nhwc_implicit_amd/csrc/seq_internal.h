@@ -78,8 +78,13 @@ struct ScanStepArgs {
     void *y;
 };
 
-// tokens a wave takes at once: its states' decays and values stay in registers
+// Tokens a wave takes at once: as many as keep the loads of the next ones under
+// way without filling the registers.
 constexpr int scan_step_tokens(int n) { return n <= 16 ? 16 : n <= 32 ? 8 : 4; }
+// The gradient keeps a step's decays and states in registers, TS * n/4 values of
+// each: 64 registers of each would spill (16 tokens of 16 states: 1115 us for
+// four sequences of 2048 with 2048 channels).
+constexpr int scan_grad_step_tokens(int n) { return n <= 8 ? 16 : n <= 16 ? 8 : 4; }
 
 hipError_t launch_scan(int dtype, const ScanArgs &a, hipStream_t st);
 hipError_t launch_scan_grad(int dtype, const ScanArgs &a, hipStream_t st);

@@ -118,7 +118,7 @@ int causal_conv_step(const causal_conv_step_problem_t *prob, int dtype, const vo
  *   initial_state and final_state [seqs][d][n] (may be NULL): fp32, dense.  The
  *             states must not overlap.
  *   y [tokens][d] dense, dtype; must not overlap the inputs.
- * 1 <= n <= 64; groups divides d.  Row strides are below 2^26.
+ * 1 <= n <= 64; groups divides d.  Row strides and d are below 2^24.
  * Long sequences are cut into chunks that run side by side, joined through the
  * workspace (selective_scan_workspace_size; 16-byte aligned; the size may be 0).
  */
