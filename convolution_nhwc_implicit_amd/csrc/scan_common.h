@@ -80,9 +80,6 @@ __device__ inline float softplus_f32(float raw)
     return raw != raw ? raw : r;  // the maximum above drops a NaN
 }
 
-// A value that every lane of the wave holds, in a scalar register.
-__device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
-
 // The chunk that a workgroup walks.
 struct Chunk {
     int s;            // sequence

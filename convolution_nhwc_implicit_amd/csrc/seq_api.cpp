@@ -82,7 +82,7 @@ constexpr int kConvMostRows = 32, kConvGradMostRows = 64;
 
 int conv_grad_plan(const causal_conv_problem_t *p, int dtype, bool states, ConvPlan *c, size_t *ws)
 {
-    *c = conv_plan(p, kConvGradBytes / bytes_of(dtype), kConvGradMostRows, states);
+    *c = conv_plan(p, conv_channels(p->d), kConvGradMostRows, states);
     *ws = up((size_t)c->run_blocks * (p->w + 1) * p->d * 4);
     return CONV2D_OK;
 }
@@ -202,7 +202,7 @@ int causal_conv(const causal_conv_problem_t *prob, int dtype, const void *x, con
     const bool rows = prob->batch.tokens > 0;
     if (!weight || (rows && (!x || !y))) return CONV2D_ERR_INVALID_ARGUMENT;
     if (!all_aligned(bytes_of(dtype), {x, weight, bias, initial_state, y, final_state})) return CONV2D_ERR_UNSUPPORTED;
-    const int v = kConvBytes / bytes_of(dtype);
+    const int v = conv_channels(prob->d);
     const ConvPlan c = conv_plan(prob, v, kConvMostRows, final_state != nullptr);
     if (ceil_div(prob->d, c.lanes * v) > kMaxGridY) return CONV2D_ERR_UNSUPPORTED;
     if (c.run_blocks + c.state_blocks == 0) return CONV2D_OK;
@@ -249,7 +249,7 @@ int causal_conv_grad(const causal_conv_problem_t *prob, int dtype, const void *d
     ConvPlan c;
     size_t need;
     conv_grad_plan(prob, dtype, dinitial != nullptr, &c, &need);
-    const int v = kConvGradBytes / bytes_of(dtype);
+    const int v = conv_channels(prob->d);
     if (ceil_div(prob->d, c.lanes * v) > kMaxGridY) return CONV2D_ERR_UNSUPPORTED;
     if (need && !workspace) return CONV2D_ERR_INVALID_ARGUMENT;
     if (workspace_bytes < need) return CONV2D_ERR_WORKSPACE_TOO_SMALL;
@@ -288,7 +288,7 @@ int causal_conv_step(const causal_conv_step_problem_t *prob, int dtype, const vo
     if (prob->rows == 0) return CONV2D_OK;
     if (!x || !weight || !y || (prob->pool > 0 && !state)) return CONV2D_ERR_INVALID_ARGUMENT;
     if (!all_aligned(bytes_of(dtype), {x, state, weight, bias, y}) || !aligned(slots, 4)) return CONV2D_ERR_UNSUPPORTED;
-    const int v = kConvGradBytes / bytes_of(dtype), lanes = lanes_for(prob->d, v);
+    const int v = kConvChannels, lanes = lanes_for(prob->d, v);
     if (ceil_div(prob->d, lanes * v) > kMaxGridY) return CONV2D_ERR_UNSUPPORTED;
     ConvStepArgs a = {prob->rows, prob->pool, prob->d, prob->silu, lanes, prob->x_row, x, weight, bias, slots, state, y};
     return status(launch_conv_step(dtype, prob->w, a,

@@ -67,6 +67,9 @@ __device__ inline void store_vec(typename E::S *p, int have, const float (&in)[V
     }
 }
 
+// A value that every lane of the wave holds, in a scalar register.
+__device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
 // ---- sequences ---------------------------------------------------------------
 // `tokens` rows hold `seqs` sequences: [seqs][len] when start is null, else
 // sequence s is rows start[s] .. start[s+1]-1.  start is device memory that the

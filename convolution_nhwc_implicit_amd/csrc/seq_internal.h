@@ -8,8 +8,8 @@ namespace cnv {
 
 // ---- causal convolution (causal_conv.hip) -------------------------------------
 constexpr int kConvUnroll = 4;    // rows whose loads are issued together
-constexpr int kConvBytes = 16;    // bytes of channels per thread: forward,
-constexpr int kConvGradBytes = 8; // and gradients and step (more live values per channel)
+constexpr int kConvChannels = 4;  // channels per thread, where there are so many
+constexpr int conv_channels(int d) { return d < kConvChannels ? 1 : kConvChannels; }
 
 struct ConvArgs {
     Seqs q;
