@@ -468,7 +468,7 @@ int fp8_matmul_workspace_size(const fp8_matmul_problem_t *prob, int dtype, size_
     if (!bytes) return CONV2D_ERR_INVALID_ARGUMENT;
     *bytes = 0;
     if (prob->m > 0 && prob->n > 0)
-        *bytes = fp8_matmul_bytes(prob->m, prob->n, fp8_matmul_plan(prob->m, prob->n, (int)ceil_div(prob->k, kFp8Block)));
+        *bytes = fp8_matmul_bytes(prob->m, prob->n, fp8_matmul_plan(prob->m, prob->n, prob->k, dtype));
     return CONV2D_OK;
 }
 
@@ -483,7 +483,7 @@ int fp8_matmul(const fp8_matmul_problem_t *prob, int dtype, const void *a, const
     if (!aligned(a, 16) || !aligned(b, 16) || !all_aligned(4, {a_scale, b_scale}) || !aligned(out, bytes_of(dtype)) ||
         !aligned(workspace, 16))
         return CONV2D_ERR_UNSUPPORTED;
-    const Fp8Plan plan = fp8_matmul_plan(prob->m, prob->n, (int)ceil_div(prob->k, kFp8Block));
+    const Fp8Plan plan = fp8_matmul_plan(prob->m, prob->n, prob->k, dtype);
     const size_t need = fp8_matmul_bytes(prob->m, prob->n, plan);
     if (need && !workspace) return CONV2D_ERR_INVALID_ARGUMENT;
     if (workspace_bytes < need) return CONV2D_ERR_WORKSPACE_TOO_SMALL;

@@ -498,7 +498,7 @@ PyObject *py_fp8_quantize(PyObject *, PyObject *const *a, Py_ssize_t n)
     c.strided(*x, "x", x->scalar_type(), x->sizes());
     c.device(*x);
     const int64_t m = x->size(0), k = x->size(1), rows = transpose ? k : m, cols = transpose ? m : k;
-    const int64_t pitch = (cols + 15) / 16 * 16;
+    const int64_t pitch = (cols + 127) / 128 * 128;  // whole lines: rows that straddle them cost the products' loads
     const c10::DeviceGuard guard(x->device());
     const Tensor q = new_tensor(*x, {rows, pitch}, at::kFloat8_e4m3fn);
     const Tensor scale = new_tensor(*x, {blocks ? blocks_of(rows) : rows, blocks_of(cols)}, at::kFloat);

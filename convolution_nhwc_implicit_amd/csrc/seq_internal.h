@@ -109,15 +109,17 @@ struct Fp8MatmulArgs {
     const float *a_scale, *b_scale;
     void *out;
     int tiles_m, tiles_n;
+    long long ldo;  // row stride of out
     int kb_split;  // blocks along k per workgroup
 };
 
 struct Fp8Plan {
     int shape, splits, per;  // tile shape; workgroups along k, and blocks of each
+    bool narrow_m, narrow_n; // the rows of a, or of b, past whole tiles go to the narrow kernel
 };
 
 hipError_t launch_fp8_quantize(int form, int dtype, const Fp8QuantArgs &a, hipStream_t st);
-Fp8Plan fp8_matmul_plan(int m, int n, int kb);
+Fp8Plan fp8_matmul_plan(int m, int n, int k, int dtype);
 size_t fp8_matmul_bytes(int m, int n, const Fp8Plan &p);
 hipError_t launch_fp8_matmul(int dtype, const Fp8MatmulArgs &a, const Fp8Plan &p, void *workspace, hipStream_t st);
 

@@ -106,7 +106,7 @@ def fp8_quantize(x, transpose=False, blocks=False):
     transpose: of x's transpose, q [k][m] and scale [k][ceil(m/128)].  blocks: a scale for every 128 x 128
     values (weights), scale [ceil(m/128)][ceil(k/128)].  Scales are the least powers of two (at least 2^-126)
     that bring a block's finite values into e4m3's range; infinities and NaN become NaN.  q's rows are padded
-    with zeros to a multiple of 16 bytes; q is a view of them."""
+    with zeros to a multiple of 128 bytes; q is a view of them."""
     return load().fp8_quantize(x, transpose, blocks)
 
 
