@@ -160,48 +160,61 @@ __global__ __launch_bounds__(256) void scan_join_kernel(ScanArgs a)
     if (a.dinitial) a.dinitial[s * per + i] = b;
 }
 
-// One token per row on pooled states: 4 lanes to a channel as above.
-template <class E, int NL>
+// One token per row on pooled states: 4 lanes to a channel as above, R rows to a
+// thread.  Bound by the states' bytes; what the rows share is loaded once, and
+// all rows' loads are under way together.
+template <class E, int NL, int R>
 __global__ __launch_bounds__(256) void scan_step_kernel(ScanStepArgs a)
 {
     using S = typename E::S;
     const int part = threadIdx.x % 4, ch = blockIdx.y * 64 + threadIdx.x / 4;
-    const long long r = blockIdx.x;
+    const int r0 = blockIdx.x * R;
     if (ch >= a.d) return;
-    const int slot = a.slots ? a.slots[r] : (int)r;
-    S *y = (S *)a.y + r * a.d + ch;
-    if (slot < 0 || slot >= a.pool) {
-        if (part == 0) *y = E::from(0.0f);
-        return;
-    }
-    const int group = ch / (a.d / a.groups);
-    float A[NL], h[NL];
-    float *state = a.state + ((long long)slot * a.d + ch) * a.n;
-    read_nl<NL>(state, a.n, part, h);
-    read_nl<NL>(a.A + (long long)ch * a.n, a.n, part, A);
-    const float x = E::to(((const S *)a.x)[r * a.x_row + ch]);
-    const float raw = E::to(((const S *)a.dt)[r * a.dt_row + ch]) + (a.dt_bias ? a.dt_bias[ch] : 0.0f);
-    const float delta = a.softplus ? softplus_f32(raw) : raw, dx = delta * x;
-    float v = 0.0f;
+    const int group = ch / (a.d / a.groups), first = part * NL, have = a.n - first;
+    float A2[NL], h[R][NL], B[R][NL], C[R][NL];
+    S x[R], dt[R], z[R];
+    float *state[R];
 #pragma unroll
-    for (int j = 0; j < NL; ++j) {
-        const int n = part * NL + j;
-        if (n < a.n) {
-            const float B = E::to(((const S *)a.B)[r * a.b_row + group * a.b_group + n]);
-            const float C = E::to(((const S *)a.C)[r * a.c_row + group * a.c_group + n]);
-            h[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(delta * (A[j] * kLog2e)), h[j], dx * B);
-            v = __builtin_fmaf(h[j], C, v);
+    for (int u = 0; u < R; ++u) {
+        const long long r = r0 + u < a.rows ? r0 + u : a.rows - 1;
+        const int slot = a.slots ? a.slots[r] : (int)r;
+        const bool mine = slot >= 0 && slot < a.pool && r0 + u < a.rows;
+        state[u] = mine ? a.state + ((long long)slot * a.d + ch) * a.n : nullptr;
+        x[u] = ((const S *)a.x)[r * a.x_row + ch];
+        dt[u] = ((const S *)a.dt)[r * a.dt_row + ch];
+        z[u] = a.z ? ((const S *)a.z)[r * a.z_row + ch] : (S)0;
+        load_vec<E, NL>((const S *)a.B + r * a.b_row + group * a.b_group + first, have, B[u]);
+        load_vec<E, NL>((const S *)a.C + r * a.c_row + group * a.c_group + first, have, C[u]);
+        if (mine) read_nl<NL>(state[u], a.n, part, h[u]);
+    }
+    read_nl<NL>(a.A + (long long)ch * a.n, a.n, part, A2);
+    const float bias = a.dt_bias ? a.dt_bias[ch] : 0.0f, D = a.D ? a.D[ch] : 0.0f;
+#pragma unroll
+    for (int j = 0; j < NL; ++j) A2[j] *= kLog2e;
+#pragma unroll
+    for (int u = 0; u < R; ++u) {
+        if (r0 + u >= a.rows) break;
+        S *y = (S *)a.y + (long long)(r0 + u) * a.d + ch;
+        if (!state[u]) {
+            if (part == 0) *y = E::from(0.0f);
+            continue;
         }
+        const float xv = E::to(x[u]), raw = E::to(dt[u]) + bias;
+        const float delta = a.softplus ? softplus_f32(raw) : raw, dx = delta * xv;
+        float v = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NL; ++j) {
+            h[u][j] = __builtin_fmaf(__builtin_amdgcn_exp2f(delta * A2[j]), h[u][j], dx * B[u][j]);
+            v = __builtin_fmaf(h[u][j], C[u][j], v);
+        }
+        write_nl<NL>(state[u], a.n, part, h[u]);
+        v = __builtin_fmaf(D, xv, quad_sum(v));
+        if (a.z) {
+            const float zv = E::to(z[u]);
+            v *= zv * sigmoid_f32(zv);
+        }
+        if (part == 0) *y = E::from(v);
     }
-    write_nl<NL>(state, a.n, part, h);
-    v = quad_sum(v);
-    if (part != 0) return;
-    if (a.D) v = __builtin_fmaf(a.D[ch], x, v);
-    if (a.z) {
-        const float z = E::to(((const S *)a.z)[r * a.z_row + ch]);
-        v *= z * sigmoid_f32(z);
-    }
-    *y = E::from(v);
 }
 
 }  // namespace
@@ -229,10 +242,13 @@ hipError_t launch_scan(int dtype, const ScanArgs &a, hipStream_t st)
 
 hipError_t launch_scan_step(int dtype, const ScanStepArgs &a, hipStream_t st)
 {
-    const dim3 grid((unsigned)a.rows, (unsigned)((a.d + 63) / 64));
+    const int blocks = (a.d + 63) / 64;
     return scan_by_type(dtype, a.n, [&](auto e, auto nl) {
         using E = decltype(e);
-        scan_step_kernel<E, decltype(nl)::value><<<grid, 256, 0, st>>>(a);
+        constexpr int NL = decltype(nl)::value, R = NL > 4 ? 2 : 4;
+        // few rows: one each, over as many compute units
+        if ((long long)a.rows * blocks < 4096) scan_step_kernel<E, NL, 1><<<dim3((unsigned)a.rows, (unsigned)blocks), 256, 0, st>>>(a);
+        else scan_step_kernel<E, NL, R><<<dim3((unsigned)((a.rows + R - 1) / R), (unsigned)blocks), 256, 0, st>>>(a);
         return hipGetLastError();
     });
 }
