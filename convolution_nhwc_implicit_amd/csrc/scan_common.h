@@ -60,6 +60,14 @@ __device__ inline float channel_sum4(float v0, float v1, float v2, float v3)
     return s + dpp<kRowRor8>(s);
 }
 
+// The value, computed here whatever becomes of it: a choice by a flag of the
+// call is then a select, where a branch would cut the code around it in pieces.
+__device__ inline float here(float v)
+{
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
 // log(1 + e^raw) = max(raw, 0) + log1p(e), e = e^-|raw| in (0, 1].  With
 // w = e / (2 + e) <= 1/3, log1p(e) = 2 atanh(w) = 2 w (1 + w^2/3 + w^4/5 + ...):
 // relative accuracy for every raw (1 + e would lose small e's bits); the first
@@ -165,11 +173,13 @@ __device__ inline __amdgpu_buffer_rsrc_t buffer_of(const void *p, uint32_t bytes
     const uint64_t u = (uint64_t)(uint32_t)uniform((int)(uint32_t)v) | (uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32;
     return __builtin_amdgcn_make_buffer_rsrc((void *)u, 0, uniform((int)bytes), 0x00020000);
 }
-// `rows` (at least 1) rows of `width` elements from element `at` of a tensor on
+// `rows` rows of `width` elements from element `at` of a tensor on; none where
+// rows is below 1
 template <class E>
 __device__ inline __amdgpu_buffer_rsrc_t rows_of(const void *p, long long at, int rows, long long row, int width)
 {
-    return buffer_of((const char *)p + at * E::kBytes, ((uint32_t)(rows - 1) * (uint32_t)row + (uint32_t)width) * E::kBytes);
+    return buffer_of((const char *)p + at * E::kBytes,
+                     rows > 0 ? ((uint32_t)(rows - 1) * (uint32_t)row + (uint32_t)width) * E::kBytes : 0u);
 }
 template <class E>
 __device__ inline typename E::S get(__amdgpu_buffer_rsrc_t r, uint32_t off)
@@ -231,12 +241,13 @@ struct Channels {
     int ch;            // this lane's channel, clamped to one that exists
     bool valid;        // whether it exists
     int part;          // lane % 4
-    __device__ inline Channels(const ScanArgs &a, int blk)
+    // `width` channels to a workgroup, 16 of them to wave `wave`
+    __device__ inline Channels(const ScanArgs &a, int blk, int width, int wave)
     {
-        const int dg = a.d / a.groups, lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+        const int dg = a.d / a.groups, lane = threadIdx.x % 64;
         block = blk;
         group = blk / a.blocks_per_group;
-        const int c = (blk % a.blocks_per_group) * kScanChannels + wave * 16 + lane / 4;
+        const int c = (blk % a.blocks_per_group) * width + wave * 16 + lane / 4;
         valid = c < dg;
         ch = group * dg + (valid ? c : dg - 1);
         part = lane % 4;
@@ -329,6 +340,19 @@ struct StageBC {
             lb[threadIdx.x] = E::to(b);
             if (lc) lc[threadIdx.x] = E::to(c);
         }
+    }
+};
+
+// The lanes' NL values of four tokens, read from LDS ahead of their use.
+template <int NL>
+struct Four {
+    float v[4][NL];
+    __device__ inline void read(const float *p, int i, int part)
+    {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int j = 0; j < NL; ++j) v[q][j] = p[(4 * i + q) * 4 * NL + part * NL + j];
     }
 };
 

@@ -5,96 +5,209 @@
 //   y[t][c] = (sum_n h[t][c][n] C[t][g(c)][n] + D[c] x[t][c]) silu(z[t][c])
 //
 // States stay in fp32 registers; only inputs and outputs cross memory.  Every
-// (t, c, n) costs one exp2 (8 cycles of a wave64) and four plain operations (4
-// each), which outweighs the bytes: the kernels are bound by the vector units.
+// (t, c, n) costs one exp2 (8 cycles of a wave64) and at least four plain
+// operations (4 each), which outweighs the bytes: bound by the vector units.
+//
+// The recurrence is linear in the state, so a workgroup's waves take successive
+// runs of TS tokens of the same 16 channels at once.  A wave scans its run from a
+// zero state, keeping each token's decay and input in registers; then the runs'
+// ends are joined through LDS (a run's decay is exp(A * the sum of its steps)),
+// and the wave scans again from its true first state, which takes no further
+// exponential.  One exponential and six plain operations a state, against two and
+// seven where sequences are cut into chunks that are walked twice.
 #include "scan_common.h"
 
 namespace cnv {
 namespace {
 
-// One chunk of one sequence for 64 channels.  LOCAL: from a zero state, only
-// the state the chunk ends with and the sum of its steps are written (the
-// decay over a chunk is exp(A * that sum)), for scan_join_kernel.
-template <class E, int NL, bool LOCAL>
-__global__ __launch_bounds__(256) void scan_kernel(ScanArgs a)
+// A wave's B and C of TS tokens as fp32 in LDS, [TS][4*NL] each: lanes take
+// neighbouring values, value k of a lane 64/(4*NL) tokens further each.
+template <class E, int NL, int TS>
+struct WaveBC {
+    static constexpr int kCount = TS * 4 * NL, kEach = (kCount + 63) / 64, kTokens = 64 / (4 * NL);
+    typename E::S b[kEach], c[kEach];
+    uint32_t boff, coff, bstep, cstep;
+    __device__ inline WaveBC(const ScanArgs &a)
+    {
+        const uint32_t lane = threadIdx.x % 64, tok = lane / (4 * NL), n = lane % (4 * NL);
+        const bool mine = (int)n < a.n;
+        boff = mine ? (tok * (uint32_t)a.bs.row + n) * E::kBytes : kNowhere;
+        coff = mine ? (tok * (uint32_t)a.cs.row + n) * E::kBytes : kNowhere;
+        bstep = kTokens * (uint32_t)a.bs.row * E::kBytes;
+        cstep = kTokens * (uint32_t)a.cs.row * E::kBytes;
+    }
+    __device__ inline void load(const ScanArgs &a, const Chunk &q, int group, int t, int rows, bool want_c)
+    {
+        const auto rb = rows_of<E>(a.B, a.bs.at(a.q, q.s, t) + group * a.b_group, rows, a.bs.row, a.n);
+        const auto rc = rows_of<E>(a.C, a.cs.at(a.q, q.s, t) + group * a.c_group, rows, a.cs.row, a.n);
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            b[k] = get<E>(rb, boff + k * bstep);
+            if (want_c) c[k] = get<E>(rc, coff + k * cstep);
+        }
+    }
+    __device__ inline void store(float *lb, float *lc, bool want_c) const
+    {
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            const int i = threadIdx.x % 64 + 64 * k;
+            lb[i] = E::to(b[k]);
+            if (want_c) lc[i] = E::to(c[k]);
+        }
+    }
+};
+
+// One chunk of one sequence for 16 channels.  LOCAL: from a zero state, only the
+// state the chunk ends with and the sum of its steps are written, for
+// scan_join_kernel.
+template <class E, int NL, int waves, bool LOCAL>
+__global__ __launch_bounds__(waves * 64, 2) void scan_kernel(ScanArgs a)
 {
     constexpr int TS = scan_step_tokens(4 * NL), G = TS / 4;
     using S = typename E::S;
-    const int slot = blockIdx.x;
+    // Each die takes a run of channel blocks, all their chunks (sequences differ
+    // in length); four neighbouring blocks of a chunk, which share lines of
+    // memory, follow one another.
+    const int blocks = a.blocks_per_group * a.groups, total = a.slots * blocks, per_die = (total + 7) / 8;
+    const int id = blockIdx.x % 8 * per_die + blockIdx.x / 8;
+    if (id >= total) return;
+    const int four = id / (4 * a.slots), wide = blocks - 4 * four < 4 ? blocks - 4 * four : 4, at4 = id - 4 * four * a.slots;
+    const int slot = at4 / wide, block = 4 * four + at4 % wide;
     const Chunk k = find_chunk(a, slot);
     if (!k.valid || (LOCAL && k.last)) return;
-    const Channels c(a, blockIdx.y);
+    const int wave = uniform(threadIdx.x / 64), lane = threadIdx.x % 64;
+    const Channels c(a, block, kScanWaveChannels, 0);
     const StateAt<NL> at(a, c);
     const int part = c.part;
     const bool odd = part & 1, high = part & 2, gated = !LOCAL && a.z;
 
-    float A2[NL], h[NL];
+    float A2[NL], first[NL];  // first: the state before the waves' next runs
     at.load(a.A, 0, A2);
 #pragma unroll
     for (int j = 0; j < NL; ++j) {
         A2[j] *= kLog2e;
-        h[j] = 0.0f;
+        first[j] = 0.0f;
     }
     if (!LOCAL) {
-        if (a.chunk_state) at.load(a.chunk_state, slot, h);
-        else if (a.initial) at.load(a.initial, k.s, h);
+        if (a.chunk_state) at.load(a.chunk_state, slot, first);
+        else if (a.initial) at.load(a.initial, k.s, first);
     }
     const float bias = a.dt_bias ? channel_load(a.dt_bias, 0, a, c) : 0.0f;
     const float D = !LOCAL && a.D ? channel_load(a.D, 0, a, c) : 0.0f;
     float sum_delta = 0.0f;
 
-    __shared__ float lb[2][TS * 4 * NL], lc[2][TS * 4 * NL];
+    extern __shared__ __align__(16) float shared[];
+    // the runs' decays and ends, double buffered: [2][waves][2][64][NL]; then the waves' B and C
+    constexpr int kEnds = waves * 2 * 64 * NL;
+    float *lb = shared + 2 * kEnds + wave * 2 * WaveBC<E, NL, TS>::kEach * 64, *lc = lb + WaveBC<E, NL, TS>::kEach * 64;
+
     const TokenAt<E> ax(c, a.xs.row), adt(c, a.dts.row), az(c, gated ? a.zs.row : 0), ay(c, a.d);
     S x[G], dt[G], z[G];
-    StageBC<E, NL, TS> bc(a);
+    WaveBC<E, NL, TS> bc(a);
+    // rows past the chunk read as zero, and a whole run past it takes no memory
     auto fetch = [&](int t) {
         const int rows = k.t1 - t < TS ? k.t1 - t : TS;
         const auto bx = rows_of<E>(a.x, a.xs.at(a.q, k.s, t), rows, a.xs.row, a.d);
         const auto bdt = rows_of<E>(a.dt, a.dts.at(a.q, k.s, t), rows, a.dts.row, a.d);
+        const auto bz = rows_of<E>(a.z, gated ? a.zs.at(a.q, k.s, t) : 0, gated ? rows : 0, a.zs.row, a.d);
 #pragma unroll
         for (int i = 0; i < G; ++i) {
             x[i] = get<E>(bx, ax[i]);
             dt[i] = get<E>(bdt, adt[i]);
+            if (!LOCAL) z[i] = get<E>(bz, az[i]);
         }
-        if (gated) {
-            const auto bz = rows_of<E>(a.z, a.zs.at(a.q, k.s, t), rows, a.zs.row, a.d);
-#pragma unroll
-            for (int i = 0; i < G; ++i) z[i] = get<E>(bz, az[i]);
-        }
-        bc.load(a, k, c.group, t, !LOCAL);
+        bc.load(a, k, c.group, t, rows, !LOCAL);
     };
-    if (k.t0 < k.t1) fetch(k.t0);
+    fetch(k.t0 + wave * TS);
     int buf = 0;
-    for (int t = k.t0; t < k.t1; t += TS, buf ^= 1) {
-        const int rem = k.t1 - t;
-        float delta[G], dx[G], xv[G], zv[G];
+    for (int t0 = k.t0; t0 < k.t1; t0 += waves * TS, buf ^= 1) {
+        const int t = t0 + wave * TS, rem = k.t1 - t;  // rem may be below 1: then no token is valid
+        float delta[G], dx[G], xv[G], zv[G], run_delta = 0.0f;
 #pragma unroll
         for (int i = 0; i < G; ++i) {
             const bool valid = c.valid && 4 * i + part < rem;
-            const float raw = E::to(dt[i]) + bias;
+            const float raw = E::to(dt[i]) + bias, soft = here(softplus_f32(raw));
             xv[i] = E::to(x[i]);
-            delta[i] = a.softplus ? softplus_f32(raw) : raw;
+            delta[i] = a.softplus ? soft : raw;
             delta[i] = valid ? delta[i] : 0.0f;  // a token that is not there leaves the state as it is
-            dx[i] = delta[i] * xv[i];
-            if (LOCAL) sum_delta += delta[i];
-            zv[i] = gated ? E::to(z[i]) : 0.0f;
+            dx[i] = valid ? delta[i] * xv[i] : 0.0f;
+            run_delta += delta[i];
+            zv[i] = LOCAL ? 0.0f : E::to(z[i]);
         }
-        bc.store(lb[buf], LOCAL ? nullptr : lc[buf]);
-        if (rem > TS) fetch(t + TS);
+        bc.store(lb, lc, !LOCAL);
+        fetch(t + waves * TS);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        run_delta = quad_sum(run_delta);
+
+        // the run from a zero state
+        float e[TS][NL], in[TS][NL], h[NL];
+#pragma unroll
+        for (int j = 0; j < NL; ++j) h[j] = 0.0f;
+        Four<NL> ahead;
+        ahead.read(lb, 0, part);
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+            const Four<NL> B = ahead;
+            if (i + 1 < G) ahead.read(lb, i + 1, part);
+            else if (!LOCAL) ahead.read(lc, 0, part);
+            __builtin_amdgcn_sched_barrier(0);
+            auto token = [&](auto qc) {
+                constexpr int Q = decltype(qc)::value;
+                const int u = 4 * i + Q;
+                const float dq = quad_bcast<Q>(delta[i]), dxq = quad_bcast<Q>(dx[i]);
+#pragma unroll
+                for (int j = 0; j < NL; ++j) {
+                    e[u][j] = __builtin_amdgcn_exp2f(dq * A2[j]);
+                    in[u][j] = dxq * B.v[Q][j];
+                    h[j] = __builtin_fmaf(e[u][j], h[j], in[u][j]);
+                }
+            };
+            token(std::integral_constant<int, 0>{});
+            token(std::integral_constant<int, 1>{});
+            token(std::integral_constant<int, 2>{});
+            token(std::integral_constant<int, 3>{});
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        // the runs' ends, and from them every run's first state
+        float *mine = shared + buf * kEnds + wave * 2 * 64 * NL + lane * NL;
+#pragma unroll
+        for (int j = 0; j < NL; ++j) {
+            mine[j] = __builtin_amdgcn_exp2f(run_delta * A2[j]);
+            mine[64 * NL + j] = h[j];
+        }
         __syncthreads();
+#pragma unroll
+        for (int w = 0; w < waves; ++w) {
+            const float *p = shared + buf * kEnds + w * 2 * 64 * NL + lane * NL;
+            if (w == wave) {
+                // one wave in `waves` takes this: a branch, not a select for each value
+#pragma unroll
+                for (int j = 0; j < NL; ++j) asm volatile("v_mov_b32 %0, %1" : "=v"(h[j]) : "v"(first[j]));
+            }
+#pragma unroll
+            for (int j = 0; j < NL; ++j) first[j] = __builtin_fmaf(p[j], first[j], p[64 * NL + j]);
+        }
+        if (LOCAL) {
+            sum_delta += run_delta;
+            continue;
+        }
+        // and the run from it
         const auto by = rows_of<E>(a.y, (long long)t * a.d, rem < TS ? rem : TS, a.d, a.d);
 #pragma unroll
         for (int i = 0; i < G; ++i) {
+            const Four<NL> C = ahead;
+            if (i + 1 < G) ahead.read(lc, i + 1, part);
+            __builtin_amdgcn_sched_barrier(0);
             float acc[4];
             auto token = [&](auto qc) {
                 constexpr int Q = decltype(qc)::value;
-                const float *pb = &lb[buf][(4 * i + Q) * 4 * NL + part * NL], *pc = &lc[buf][(4 * i + Q) * 4 * NL + part * NL];
-                const float dq = quad_bcast<Q>(delta[i]), dxq = quad_bcast<Q>(dx[i]);
+                const int u = 4 * i + Q;
                 float v = 0.0f;
 #pragma unroll
                 for (int j = 0; j < NL; ++j) {
-                    h[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(dq * A2[j]), h[j], dxq * pb[j]);
-                    if (!LOCAL) v = __builtin_fmaf(h[j], pc[j], v);
+                    h[j] = __builtin_fmaf(e[u][j], h[j], in[u][j]);
+                    v = __builtin_fmaf(h[j], C.v[Q][j], v);
                 }
                 acc[Q] = v;
             };
@@ -102,18 +215,25 @@ __global__ __launch_bounds__(256) void scan_kernel(ScanArgs a)
             token(std::integral_constant<int, 1>{});
             token(std::integral_constant<int, 2>{});
             token(std::integral_constant<int, 3>{});
-            if (!LOCAL) {
-                float v = __builtin_fmaf(D, xv[i], quad_scatter_sum(acc[0], acc[1], acc[2], acc[3], odd, high));
-                if (gated) v *= zv[i] * sigmoid_f32(zv[i]);
-                put<E>(by, ay[i], v);
-            }
+            const float v = __builtin_fmaf(D, xv[i], quad_scatter_sum(acc[0], acc[1], acc[2], acc[3], odd, high));
+            const float w = here(v * (zv[i] * sigmoid_f32(zv[i])));
+            put<E>(by, ay[i], gated ? w : v);
+            __builtin_amdgcn_sched_barrier(0);
         }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
     }
     if (LOCAL) {
-        at.store(a.chunk_state, slot, h);
-        channel_store(a.chunk_delta, slot, a, c, quad_sum(sum_delta));
-    } else if (a.final_state && k.last) {
-        at.store(a.final_state, k.s, h);
+        if (wave == 0) at.store(a.chunk_state, slot, first);
+        // the waves' sums of steps, in order
+        __syncthreads();
+        shared[wave * 64 + lane] = sum_delta;
+        __syncthreads();
+        float v = 0.0f;
+        for (int w = 0; w < waves; ++w) v += shared[w * 64 + lane];
+        if (wave == 0) channel_store(a.chunk_delta, slot, a, c, v);
+    } else if (a.final_state && k.last && wave == 0) {
+        at.store(a.final_state, k.s, first);
     }
 }
 
@@ -225,18 +345,34 @@ void launch_scan_join(const ScanArgs &a, hipStream_t st)
     scan_join_kernel<<<dim3((unsigned)a.q.seqs, (unsigned)((per + 255) / 256)), 256, 0, st>>>(a);
 }
 
-hipError_t launch_scan(int dtype, const ScanArgs &a, hipStream_t st)
+hipError_t launch_scan(int dtype, const ScanArgs &a, int waves, hipStream_t st)
 {
-    const dim3 grid((unsigned)a.slots, (unsigned)(a.blocks_per_group * a.groups));
+    const long long total = (long long)a.slots * a.blocks_per_group * a.groups;
+    const dim3 grid((unsigned)((total + 7) / 8 * 8));
     return scan_by_type(dtype, a.n, [&](auto e, auto nl) {
         using E = decltype(e);
-        constexpr int NL = decltype(nl)::value;
-        if (a.chunk_state) {
-            scan_kernel<E, NL, true><<<grid, 256, 0, st>>>(a);
-            launch_scan_join(a, st);
-        }
-        scan_kernel<E, NL, false><<<grid, 256, 0, st>>>(a);
-        return hipGetLastError();
+        constexpr int NL = decltype(nl)::value, TS = scan_step_tokens(4 * NL);
+        auto run = [&](auto wc) {
+            constexpr int W = decltype(wc)::value, lds = W * (4 * NL * 64 + 2 * WaveBC<E, NL, TS>::kEach * 64) * 4;
+            auto launch = [&](auto *kernel) {
+                if (lds > 64 << 10) {
+                    const hipError_t r = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+                    if (r != hipSuccess) return r;
+                }
+                kernel<<<grid, W * 64, lds, st>>>(a);
+                return hipGetLastError();
+            };
+            if (a.chunk_state) {
+                const hipError_t r = launch(scan_kernel<E, NL, W, true>);
+                if (r != hipSuccess) return r;
+                launch_scan_join(a, st);
+            }
+            return launch(scan_kernel<E, NL, W, false>);
+        };
+        if (waves == 1) return run(std::integral_constant<int, 1>{});
+        if (waves == 2) return run(std::integral_constant<int, 2>{});
+        if (waves == 4) return run(std::integral_constant<int, 4>{});
+        return run(std::integral_constant<int, 8>{});
     });
 }
 

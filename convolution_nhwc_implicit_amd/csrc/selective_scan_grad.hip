@@ -38,24 +38,21 @@ struct Tokens {
         : ax(c, a.xs.row), adt(c, a.dts.row), az(c, a.z ? a.zs.row : 0), ady(c, a.dys.row)
     {
     }
+    // without z its rows read as zero
     __device__ inline void fetch(const ScanArgs &a, const Chunk &k, int t, bool grad)
     {
         const int rows = k.t1 - t < TS ? k.t1 - t : TS;
         const auto bx = rows_of<E>(a.x, a.xs.at(a.q, k.s, t), rows, a.xs.row, a.d);
         const auto bdt = rows_of<E>(a.dt, a.dts.at(a.q, k.s, t), rows, a.dts.row, a.d);
+        const auto bdy = rows_of<E>(a.dy, a.dys.at(a.q, k.s, t), rows, a.dys.row, a.d);
+        const auto bz = rows_of<E>(a.z, a.z ? a.zs.at(a.q, k.s, t) : 0, a.z ? rows : 0, a.zs.row, a.d);
 #pragma unroll
         for (int i = 0; i < G; ++i) {
             x[i] = get<E>(bx, ax[i]);
             dt[i] = get<E>(bdt, adt[i]);
+            if (grad) dy[i] = get<E>(bdy, ady[i]);
+            if (grad) z[i] = get<E>(bz, az[i]);
         }
-        if (!grad) return;
-        const auto bdy = rows_of<E>(a.dy, a.dys.at(a.q, k.s, t), rows, a.dys.row, a.d);
-#pragma unroll
-        for (int i = 0; i < G; ++i) dy[i] = get<E>(bdy, ady[i]);
-        if (!a.z) return;
-        const auto bz = rows_of<E>(a.z, a.zs.at(a.q, k.s, t), rows, a.zs.row, a.d);
-#pragma unroll
-        for (int i = 0; i < G; ++i) z[i] = get<E>(bz, az[i]);
     }
 };
 
@@ -66,7 +63,7 @@ __global__ __launch_bounds__(256) void scan_keep_kernel(ScanArgs a)
     const int slot = blockIdx.x;
     const Chunk k = find_chunk(a, slot);
     if (!k.valid) return;
-    const Channels c(a, blockIdx.y);
+    const Channels c(a, blockIdx.y, kScanChannels, threadIdx.x / 64);
     const StateAt<NL> at(a, c);
     const int part = c.part;
     float A2[NL], h[NL], P[NL], back[NL];
@@ -98,18 +95,15 @@ __global__ __launch_bounds__(256) void scan_keep_kernel(ScanArgs a)
 #pragma unroll
         for (int i = 0; i < G; ++i) {
             const bool valid = c.valid && 4 * i + part < rem;
-            const float raw = E::to(in.dt[i]) + bias;
-            delta[i] = a.softplus ? softplus_f32(raw) : raw;
+            const float raw = E::to(in.dt[i]) + bias, soft = here(softplus_f32(raw));
+            delta[i] = a.softplus ? soft : raw;
             delta[i] = valid ? delta[i] : 0.0f;
-            dx[i] = delta[i] * E::to(in.x[i]);
+            dx[i] = valid ? delta[i] * E::to(in.x[i]) : 0.0f;
             step_delta += delta[i];
             g[i] = 0.0f;
             if (CARRY) {
-                g[i] = E::to(in.dy[i]);
-                if (a.z) {
-                    const float z = E::to(in.z[i]);
-                    g[i] *= z * sigmoid_f32(z);
-                }
+                const float z = E::to(in.z[i]), dy = E::to(in.dy[i]), through = here(dy * (z * sigmoid_f32(z)));
+                g[i] = a.z ? through : dy;
                 g[i] = valid ? g[i] : 0.0f;  // an expanded tensor's rows (stride 0) all lie in range
             }
         }
@@ -120,19 +114,27 @@ __global__ __launch_bounds__(256) void scan_keep_kernel(ScanArgs a)
             bc.load(a, k, c.group, t + TS, CARRY);
         }
         __syncthreads();
+        Four<NL> nb, nc;
+        nb.read(lb[buf], 0, part);
+        if (CARRY) nc.read(lc[buf], 0, part);
 #pragma unroll
         for (int i = 0; i < G; ++i) {
+            const Four<NL> B = nb, C = nc;
+            if (i + 1 < G) {
+                nb.read(lb[buf], i + 1, part);
+                if (CARRY) nc.read(lc[buf], i + 1, part);
+            }
+            __builtin_amdgcn_sched_barrier(0);
             auto token = [&](auto qc) {
                 constexpr int Q = decltype(qc)::value;
-                const float *pb = &lb[buf][(4 * i + Q) * 4 * NL + part * NL], *pc = &lc[buf][(4 * i + Q) * 4 * NL + part * NL];
                 const float dq = quad_bcast<Q>(delta[i]), dxq = quad_bcast<Q>(dx[i]), gq = quad_bcast<Q>(g[i]);
 #pragma unroll
                 for (int j = 0; j < NL; ++j) {
                     const float e = __builtin_amdgcn_exp2f(dq * A2[j]);
-                    h[j] = __builtin_fmaf(e, h[j], dxq * pb[j]);
+                    h[j] = __builtin_fmaf(e, h[j], dxq * B.v[Q][j]);
                     if (CARRY) {
                         P[j] *= e;
-                        back[j] = __builtin_fmaf(P[j], gq * pc[j], back[j]);
+                        back[j] = __builtin_fmaf(P[j], gq * C.v[Q][j], back[j]);
                     }
                 }
             };
@@ -140,6 +142,7 @@ __global__ __launch_bounds__(256) void scan_keep_kernel(ScanArgs a)
             token(std::integral_constant<int, 1>{});
             token(std::integral_constant<int, 2>{});
             token(std::integral_constant<int, 3>{});
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
     if (CARRY) {
@@ -155,7 +158,7 @@ __global__ __launch_bounds__(256, NL > 8 ? 1 : 2) void scan_back_kernel(ScanArgs
     constexpr int TS = scan_grad_step_tokens(4 * NL), G = TS / 4, N4 = 4 * NL;
     const int slot = blockIdx.x, tid = threadIdx.x;
     const Chunk k = find_chunk(a, slot);
-    const Channels c(a, blockIdx.y);
+    const Channels c(a, blockIdx.y, kScanChannels, threadIdx.x / 64);
     const StateAt<NL> at(a, c);
     const int part = c.part, row = tid % 64 / 16, wave = tid / 64;
     const bool odd = part & 1, high = part & 2;
@@ -200,15 +203,17 @@ __global__ __launch_bounds__(256, NL > 8 ? 1 : 2) void scan_back_kernel(ScanArgs
         for (int i = 0; i < G; ++i) {
             const bool valid = c.valid && 4 * i + part < rem;
             const float raw = E::to(in.dt[i]) + bias;
+            const float soft = here(softplus_f32(raw)), sig = here(sigmoid_f32(raw));
             xv[i] = E::to(in.x[i]);
-            delta[i] = a.softplus ? softplus_f32(raw) : raw;
-            sig_raw[i] = a.softplus ? sigmoid_f32(raw) : 1.0f;
+            delta[i] = a.softplus ? soft : raw;
+            sig_raw[i] = a.softplus ? sig : 1.0f;
             sig_raw[i] = valid ? sig_raw[i] : 0.0f;  // so that ddt, whose sum is ddt_bias, is 0 where there is no token
             delta[i] = valid ? delta[i] : 0.0f;
-            dx[i] = delta[i] * xv[i];
+            dx[i] = valid ? delta[i] * xv[i] : 0.0f;
             dyv[i] = E::to(in.dy[i]);
-            zv[i] = a.z ? E::to(in.z[i]) : 0.0f;
-            g[i] = a.z ? dyv[i] * (zv[i] * sigmoid_f32(zv[i])) : dyv[i];
+            zv[i] = E::to(in.z[i]);
+            const float through = here(dyv[i] * (zv[i] * sigmoid_f32(zv[i])));
+            g[i] = a.z ? through : dyv[i];
             g[i] = valid ? g[i] : 0.0f;
         }
 #pragma unroll
@@ -221,8 +226,18 @@ __global__ __launch_bounds__(256, NL > 8 ? 1 : 2) void scan_back_kernel(ScanArgs
         __syncthreads();
 
         float e[TS][NL], h[TS][NL], ys[G];
+        Four<NL> nb, nc;
+        nb.read(lb, 0, part);
+        nc.read(lc, 0, part);
 #pragma unroll
         for (int i = 0; i < G; ++i) {
+            const Four<NL> B = nb, C = nc;
+            // the next group's, or for the walk back the last one's again
+            if (i + 1 < G) {
+                nb.read(lb, i + 1, part);
+                nc.read(lc, i + 1, part);
+            }
+            __builtin_amdgcn_sched_barrier(0);
             float acc[4];
             auto token = [&](auto qc) {
                 constexpr int Q = decltype(qc)::value;
@@ -232,8 +247,8 @@ __global__ __launch_bounds__(256, NL > 8 ? 1 : 2) void scan_back_kernel(ScanArgs
 #pragma unroll
                 for (int j = 0; j < NL; ++j) {
                     e[u][j] = __builtin_amdgcn_exp2f(dq * (A[j] * kLog2e));
-                    h[u][j] = __builtin_fmaf(e[u][j], u ? h[u - 1][j] : h0[j], dxq * lb[u * N4 + part * NL + j]);
-                    v = __builtin_fmaf(h[u][j], lc[u * N4 + part * NL + j], v);
+                    h[u][j] = __builtin_fmaf(e[u][j], u ? h[u - 1][j] : h0[j], dxq * B.v[Q][j]);
+                    v = __builtin_fmaf(h[u][j], C.v[Q][j], v);
                 }
                 acc[Q] = v;
             };
@@ -242,12 +257,14 @@ __global__ __launch_bounds__(256, NL > 8 ? 1 : 2) void scan_back_kernel(ScanArgs
             token(std::integral_constant<int, 2>{});
             token(std::integral_constant<int, 3>{});
             ys[i] = quad_scatter_sum(acc[0], acc[1], acc[2], acc[3], odd, high);
-            __builtin_amdgcn_sched_barrier(0);  // else every token's B and C are read ahead, and registers spill
+            __builtin_amdgcn_sched_barrier(0);
         }
         const auto bdu = rows_of<E>(a.du, (long long)t * a.d, rem, a.d, a.d);
+        const auto bdz = rows_of<E>(a.dz, (long long)t * a.d, a.z ? rem : 0, a.d, a.d);  // without z nothing is written
         const auto bddt = rows_of<E>(a.ddt, (long long)t * a.d, rem, a.d, a.d);
 #pragma unroll
         for (int i = G - 1; i >= 0; --i) {
+            const Four<NL> B = nb, C = nc;  // of group i: the last group's are still there
             float inner[4], along[4], vb[NL][4], vc[NL][4];
             auto token = [&](auto qc) {
                 constexpr int Q = decltype(qc)::value;
@@ -256,10 +273,10 @@ __global__ __launch_bounds__(256, NL > 8 ? 1 : 2) void scan_back_kernel(ScanArgs
                 inner[Q] = along[Q] = 0.0f;
 #pragma unroll
                 for (int j = 0; j < NL; ++j) {
-                    const float dh = __builtin_fmaf(gq, lc[u * N4 + part * NL + j], carry[j]);
+                    const float dh = __builtin_fmaf(gq, C.v[Q][j], carry[j]);
                     vc[j][Q] = gq * h[u][j];
                     vb[j][Q] = dxq * dh;
-                    inner[Q] = __builtin_fmaf(dh, lb[u * N4 + part * NL + j], inner[Q]);
+                    inner[Q] = __builtin_fmaf(dh, B.v[Q][j], inner[Q]);
                     carry[j] = dh * e[u][j];
                     const float b = carry[j] * (u ? h[u - 1][j] : h0[j]);
                     along[Q] = __builtin_fmaf(b, A[j], along[Q]);
@@ -271,14 +288,17 @@ __global__ __launch_bounds__(256, NL > 8 ? 1 : 2) void scan_back_kernel(ScanArgs
             token(std::integral_constant<int, 1>{});
             token(std::integral_constant<int, 0>{});
             __builtin_amdgcn_sched_barrier(0);
+            if (i > 0) {
+                nb.read(lb, i - 1, part);
+                nc.read(lc, i - 1, part);
+            }
 #pragma unroll
             for (int j = 0; j < NL; ++j) {
                 const float tb = channel_sum4(vb[j][0], vb[j][1], vb[j][2], vb[j][3]);
                 const float tc = channel_sum4(vc[j][0], vc[j][1], vc[j][2], vc[j][3]);
-                if (tid % 16 < 4) {
-                    sb[wave][(4 * i + row) * N4 + part * NL + j] = tb;
-                    sc[wave][(4 * i + row) * N4 + part * NL + j] = tc;
-                }
+                // the four quads of a row write the same value to the same place
+                sb[wave][(4 * i + row) * N4 + part * NL + j] = tb;
+                sc[wave][(4 * i + row) * N4 + part * NL + j] = tc;
             }
             const float in_sum = quad_scatter_sum(inner[0], inner[1], inner[2], inner[3], odd, high);
             const float al_sum = quad_scatter_sum(along[0], along[1], along[2], along[3], odd, high);
@@ -287,11 +307,8 @@ __global__ __launch_bounds__(256, NL > 8 ? 1 : 2) void scan_back_kernel(ScanArgs
             sum_bias += draw;
             put<E>(bdu, ao[i], __builtin_fmaf(delta[i], in_sum, D * g[i]));
             put<E>(bddt, ao[i], draw);
-            if (a.z) {
-                const float sg = sigmoid_f32(zv[i]), yv = __builtin_fmaf(D, xv[i], ys[i]);
-                put<E>(rows_of<E>(a.dz, (long long)t * a.d, rem, a.d, a.d), ao[i],
-                       dyv[i] * yv * (sg * (1.0f + zv[i] * (1.0f - sg))));
-            }
+            const float sg = sigmoid_f32(zv[i]), yv = __builtin_fmaf(D, xv[i], ys[i]);
+            put<E>(bdz, ao[i], dyv[i] * yv * (sg * (1.0f + zv[i] * (1.0f - sg))));
         }
         __syncthreads();
         if (tid < TS * N4) {

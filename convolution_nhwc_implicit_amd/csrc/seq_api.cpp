@@ -110,28 +110,34 @@ int check_scan(const selective_scan_problem_t *p, int dtype, bool grad)
         if (r == CONV2D_OK) r = check_stride(*s);
     if (r == CONV2D_OK && grad) r = check_stride(p->dy);
     if (r == CONV2D_OK && (p->b_group < 0 || p->c_group < 0)) r = CONV2D_ERR_INVALID_ARGUMENT;
-    if (r == CONV2D_OK && ceil_div(p->d / p->groups, kScanChannels) * p->groups > kMaxGridY) r = CONV2D_ERR_UNSUPPORTED;
+    if (r == CONV2D_OK && ceil_div(p->d / p->groups, kScanWaveChannels) * p->groups > kMaxGridY) r = CONV2D_ERR_UNSUPPORTED;
     return r;
 }
 
 struct ScanPlan {
-    int blocks_per_group, chunk, chunks, slots;
+    int blocks_per_group, chunk, chunks, slots, waves;
     bool joined;  // sequences are cut into more than one chunk
     size_t state, delta, check, check_delta, part_B;  // bytes
 };
 
-// Tokens per chunk: whole sequences when their workgroups fill the chip by
-// themselves, else pieces that do.  `want` is the number of workgroups to reach.
-void scan_plan(const selective_scan_problem_t *p, long long want, bool grad, ScanPlan *s)
+// Tokens per chunk.  Forward: a sequence's workgroups (16 channels, up to 8
+// waves) walk it whole where they give the chip a wave per SIMD; below that
+// chunks, though walked twice, take less time.  Gradient (64 channels, 4 waves):
+// two workgroups to a compute unit.
+void scan_plan(const selective_scan_problem_t *p, bool grad, ScanPlan *s)
 {
     const seq_batch_t &b = p->batch;
-    s->blocks_per_group = (int)ceil_div(p->d / p->groups, kScanChannels);
-    const long long blocks = (long long)s->blocks_per_group * p->groups;
+    const int ts = grad ? scan_grad_step_tokens(p->n) : scan_step_tokens(p->n);
+    s->blocks_per_group = (int)ceil_div(p->d / p->groups, grad ? kScanChannels : kScanWaveChannels);
+    const long long blocks = (long long)s->blocks_per_group * p->groups, walks = blocks * b.seqs;
     const long long longest = b.seq_start ? b.tokens : b.len;
     long long chunk = std::max<long long>(ceil_div(longest, 16) * 16, 16);
-    if (blocks * b.seqs < want) {
-        const long long pieces = std::max<long long>(1, want / blocks);
-        chunk = std::min(chunk, std::max<long long>(64, ceil_div(ceil_div(b.tokens, pieces), 16) * 16));
+    s->waves = 8;
+    while (s->waves > 1 && (s->waves / 2 * ts >= longest || walks * (s->waves / 2) >= 2 * 4 * kCUs)) s->waves /= 2;
+    const long long want = grad ? 2 * kCUs : 2 * 4 * kCUs / s->waves;
+    if (grad ? walks < want : 2 * walks < want) {
+        const long long pieces = std::max<long long>(1, want / blocks), least = grad ? 64 : s->waves * ts;
+        chunk = std::min(chunk, std::max<long long>(least, ceil_div(ceil_div(b.tokens, pieces), 16) * 16));
     }
     s->chunk = (int)std::min<long long>(chunk, 1 << 30);
     s->chunks = std::max(1, (int)ceil_div(b.len, s->chunk));
@@ -142,14 +148,12 @@ void scan_plan(const selective_scan_problem_t *p, long long want, bool grad, Sca
     s->delta = up(s->slots * d);
     s->check = s->check_delta = s->part_B = 0;
     if (grad) {
-        const long long steps = b.tokens / scan_grad_step_tokens(p->n) + s->slots + 1;  // scan_keep_index
+        const long long steps = b.tokens / ts + s->slots + 1;  // scan_keep_index
         s->check = up(steps * dn);
         s->check_delta = up(steps * d);
         s->part_B = up((size_t)blocks * b.tokens * p->n * 4);
     }
 }
-
-constexpr long long kScanWorkgroups = 1024, kScanGradWorkgroups = 512;
 
 size_t scan_bytes(const ScanPlan &s, bool grad)
 {
@@ -302,7 +306,7 @@ int selective_scan_workspace_size(const selective_scan_problem_t *prob, int dtyp
     if (r != CONV2D_OK) return r;
     if (!bytes) return CONV2D_ERR_INVALID_ARGUMENT;
     ScanPlan s;
-    scan_plan(prob, kScanWorkgroups, false, &s);
+    scan_plan(prob, false, &s);
     *bytes = scan_bytes(s, false);
     return CONV2D_OK;
 }
@@ -320,7 +324,7 @@ int selective_scan(const selective_scan_problem_t *prob, int dtype, const void *
         !all_aligned(4, {A, D, dt_bias, initial_state, final_state}) || !aligned(workspace, 16))
         return CONV2D_ERR_UNSUPPORTED;
     ScanPlan s;
-    scan_plan(prob, kScanWorkgroups, false, &s);
+    scan_plan(prob, false, &s);
     const size_t need = scan_bytes(s, false);
     if (need && !workspace) return CONV2D_ERR_INVALID_ARGUMENT;
     if (workspace_bytes < need) return CONV2D_ERR_WORKSPACE_TOO_SMALL;
@@ -342,7 +346,7 @@ int selective_scan(const selective_scan_problem_t *prob, int dtype, const void *
         a.chunk_state = w.take(s.state);
         a.chunk_delta = w.take(s.delta);
     }
-    return status(launch_scan(dtype, a, (hipStream_t)stream));
+    return status(launch_scan(dtype, a, s.waves, (hipStream_t)stream));
 }
 
 int selective_scan_grad_workspace_size(const selective_scan_problem_t *prob, int dtype, size_t *bytes)
@@ -351,7 +355,7 @@ int selective_scan_grad_workspace_size(const selective_scan_problem_t *prob, int
     if (r != CONV2D_OK) return r;
     if (!bytes) return CONV2D_ERR_INVALID_ARGUMENT;
     ScanPlan s;
-    scan_plan(prob, kScanGradWorkgroups, true, &s);
+    scan_plan(prob, true, &s);
     *bytes = scan_bytes(s, true);
     return CONV2D_OK;
 }
@@ -373,7 +377,7 @@ int selective_scan_grad(const selective_scan_problem_t *prob, int dtype, const v
         !aligned(workspace, 16))
         return CONV2D_ERR_UNSUPPORTED;
     ScanPlan s;
-    scan_plan(prob, kScanGradWorkgroups, true, &s);
+    scan_plan(prob, true, &s);
     if (workspace_bytes < scan_bytes(s, true)) return CONV2D_ERR_WORKSPACE_TOO_SMALL;
     if (prob->batch.tokens * prob->groups * prob->n > kMaxRows * 128) return CONV2D_ERR_UNSUPPORTED;
     ScanArgs a = scan_args(prob, s);

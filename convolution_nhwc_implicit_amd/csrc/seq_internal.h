@@ -38,7 +38,8 @@ hipError_t launch_conv_grad(int dtype, int w, const ConvArgs &a, dim3 grid, hipS
 hipError_t launch_conv_step(int dtype, int w, const ConvStepArgs &a, dim3 grid, hipStream_t st);
 
 // ---- selective scan (selective_scan.hip, selective_scan_grad.hip) ----------------
-constexpr int kScanChannels = 64;  // channels of a workgroup (16 to a wave)
+constexpr int kScanWaveChannels = 16;  // channels of a wave, and of a workgroup of the forward pass
+constexpr int kScanChannels = 64;      // channels of a workgroup of the gradient
 
 struct ScanArgs {
     Seqs q;
@@ -86,7 +87,7 @@ constexpr int scan_step_tokens(int n) { return n <= 16 ? 16 : n <= 32 ? 8 : 4; }
 // four sequences of 2048 with 2048 channels).
 constexpr int scan_grad_step_tokens(int n) { return n <= 8 ? 16 : n <= 16 ? 8 : 4; }
 
-hipError_t launch_scan(int dtype, const ScanArgs &a, hipStream_t st);
+hipError_t launch_scan(int dtype, const ScanArgs &a, int waves, hipStream_t st);
 hipError_t launch_scan_grad(int dtype, const ScanArgs &a, hipStream_t st);
 hipError_t launch_scan_step(int dtype, const ScanStepArgs &a, hipStream_t st);
 
