@@ -173,14 +173,25 @@ __device__ inline __amdgpu_buffer_rsrc_t buffer_of(const void *p, uint32_t bytes
     const uint64_t u = (uint64_t)(uint32_t)uniform((int)(uint32_t)v) | (uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32;
     return __builtin_amdgcn_make_buffer_rsrc((void *)u, 0, uniform((int)bytes), 0x00020000);
 }
-// `rows` rows of `width` elements from element `at` of a tensor on; none where
-// rows is below 1
+// A tensor of rows of `width` elements, walked a step at a time: the address of
+// the step's first row stays in scalar registers.
 template <class E>
-__device__ inline __amdgpu_buffer_rsrc_t rows_of(const void *p, long long at, int rows, long long row, int width)
-{
-    return buffer_of((const char *)p + at * E::kBytes,
-                     rows > 0 ? ((uint32_t)(rows - 1) * (uint32_t)row + (uint32_t)width) * E::kBytes : 0u);
-}
+struct Stream {
+    uint64_t p;
+    uint32_t row, width;  // bytes
+    __device__ inline Stream(const void *base, long long at, long long r, int w)
+        : p((uint64_t)base + at * E::kBytes), row((uint32_t)r * E::kBytes), width(base ? (uint32_t)w * E::kBytes : 0u)
+    {
+    }
+    // the first `rows` rows from here; none where rows is below 1, or of no tensor
+    __device__ inline __amdgpu_buffer_rsrc_t rows(int n) const
+    {
+        const uint32_t bytes = (uint32_t)(n - 1) * row + width;
+        return buffer_of((const void *)p, n > 0 && width ? bytes : 0u);
+    }
+    __device__ inline void advance(int n) { p += (long long)n * row; }
+};
+
 template <class E>
 __device__ inline typename E::S get(__amdgpu_buffer_rsrc_t r, uint32_t off)
 {
@@ -321,18 +332,25 @@ struct StageBC {
     static_assert(kCount <= 256, "a value per thread");
     typename E::S b, c;
     uint32_t boff, coff;
-    __device__ inline StageBC(const ScanArgs &a)
+    Stream<E> sb, sc;
+    __device__ inline StageBC(const ScanArgs &a, const Chunk &k, int group, int t)
+        : sb(a.B, a.bs.at(a.q, k.s, t) + group * a.b_group, a.bs.row, a.n),
+          sc(a.C, a.cs.at(a.q, k.s, t) + group * a.c_group, a.cs.row, a.n)
     {
         const uint32_t tok = threadIdx.x / (4 * NL), n = threadIdx.x % (4 * NL);
         const bool mine = threadIdx.x < kCount && (int)n < a.n;
-        boff = mine ? (tok * (uint32_t)a.bs.row + n) * E::kBytes : kNowhere;
-        coff = mine ? (tok * (uint32_t)a.cs.row + n) * E::kBytes : kNowhere;
+        boff = mine ? tok * sb.row + n * E::kBytes : kNowhere;
+        coff = mine ? tok * sc.row + n * E::kBytes : kNowhere;
     }
-    __device__ inline void load(const ScanArgs &a, const Chunk &k, int group, int t, bool want_c)
+    __device__ inline void load(int rows, bool want_c)
     {
-        const int rows = k.t1 - t < TS ? k.t1 - t : TS;
-        b = get<E>(rows_of<E>(a.B, a.bs.at(a.q, k.s, t) + group * a.b_group, rows, a.bs.row, a.n), boff);
-        if (want_c) c = get<E>(rows_of<E>(a.C, a.cs.at(a.q, k.s, t) + group * a.c_group, rows, a.cs.row, a.n), coff);
+        b = get<E>(sb.rows(rows), boff);
+        if (want_c) c = get<E>(sc.rows(rows), coff);
+    }
+    __device__ inline void advance(int n)
+    {
+        sb.advance(n);
+        sc.advance(n);
     }
     __device__ inline void store(float *lb, float *lc) const
     {

@@ -26,24 +26,24 @@ template <class E, int NL, int TS>
 struct WaveBC {
     static constexpr int kCount = TS * 4 * NL, kEach = (kCount + 63) / 64, kTokens = 64 / (4 * NL);
     typename E::S b[kEach], c[kEach];
-    uint32_t boff, coff, bstep, cstep;
-    __device__ inline WaveBC(const ScanArgs &a)
+    uint32_t boff, coff;
+    Stream<E> sb, sc;
+    __device__ inline WaveBC(const ScanArgs &a, const Chunk &q, int group, int t)
+        : sb(a.B, a.bs.at(a.q, q.s, t) + group * a.b_group, a.bs.row, a.n),
+          sc(a.C, a.cs.at(a.q, q.s, t) + group * a.c_group, a.cs.row, a.n)
     {
         const uint32_t lane = threadIdx.x % 64, tok = lane / (4 * NL), n = lane % (4 * NL);
         const bool mine = (int)n < a.n;
-        boff = mine ? (tok * (uint32_t)a.bs.row + n) * E::kBytes : kNowhere;
-        coff = mine ? (tok * (uint32_t)a.cs.row + n) * E::kBytes : kNowhere;
-        bstep = kTokens * (uint32_t)a.bs.row * E::kBytes;
-        cstep = kTokens * (uint32_t)a.cs.row * E::kBytes;
+        boff = mine ? tok * sb.row + n * E::kBytes : kNowhere;
+        coff = mine ? tok * sc.row + n * E::kBytes : kNowhere;
     }
-    __device__ inline void load(const ScanArgs &a, const Chunk &q, int group, int t, int rows, bool want_c)
+    __device__ inline void load(int rows, bool want_c)
     {
-        const auto rb = rows_of<E>(a.B, a.bs.at(a.q, q.s, t) + group * a.b_group, rows, a.bs.row, a.n);
-        const auto rc = rows_of<E>(a.C, a.cs.at(a.q, q.s, t) + group * a.c_group, rows, a.cs.row, a.n);
+        const auto rb = sb.rows(rows), rc = sc.rows(rows);
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
-            b[k] = get<E>(rb, boff + k * bstep);
-            if (want_c) c[k] = get<E>(rc, coff + k * cstep);
+            b[k] = get<E>(rb, boff + k * kTokens * sb.row);
+            if (want_c) c[k] = get<E>(rc, coff + k * kTokens * sc.row);
         }
     }
     __device__ inline void store(float *lb, float *lc, bool want_c) const
@@ -102,23 +102,29 @@ __global__ __launch_bounds__(waves * 64, 2) void scan_kernel(ScanArgs a)
     float *lb = shared + 2 * kEnds + wave * 2 * WaveBC<E, NL, TS>::kEach * 64, *lc = lb + WaveBC<E, NL, TS>::kEach * 64;
 
     const TokenAt<E> ax(c, a.xs.row), adt(c, a.dts.row), az(c, gated ? a.zs.row : 0), ay(c, a.d);
+    const int start = k.t0 + wave * TS;
+    Stream<E> sx(a.x, a.xs.at(a.q, k.s, start), a.xs.row, a.d), sdt(a.dt, a.dts.at(a.q, k.s, start), a.dts.row, a.d);
+    Stream<E> sz(gated ? a.z : nullptr, a.zs.at(a.q, k.s, start), a.zs.row, a.d), sy(a.y, (long long)start * a.d, a.d, a.d);
     S x[G], dt[G], z[G];
-    WaveBC<E, NL, TS> bc(a);
+    WaveBC<E, NL, TS> bc(a, k, c.group, start);
     // rows past the chunk read as zero, and a whole run past it takes no memory
-    auto fetch = [&](int t) {
-        const int rows = k.t1 - t < TS ? k.t1 - t : TS;
-        const auto bx = rows_of<E>(a.x, a.xs.at(a.q, k.s, t), rows, a.xs.row, a.d);
-        const auto bdt = rows_of<E>(a.dt, a.dts.at(a.q, k.s, t), rows, a.dts.row, a.d);
-        const auto bz = rows_of<E>(a.z, gated ? a.zs.at(a.q, k.s, t) : 0, gated ? rows : 0, a.zs.row, a.d);
+    auto fetch = [&](int rem) {
+        const int rows = rem < TS ? rem : TS;
+        const auto bx = sx.rows(rows), bdt = sdt.rows(rows), bz = sz.rows(rows);
 #pragma unroll
         for (int i = 0; i < G; ++i) {
             x[i] = get<E>(bx, ax[i]);
             dt[i] = get<E>(bdt, adt[i]);
             if (!LOCAL) z[i] = get<E>(bz, az[i]);
         }
-        bc.load(a, k, c.group, t, rows, !LOCAL);
+        bc.load(rows, !LOCAL);
+        sx.advance(waves * TS);
+        sdt.advance(waves * TS);
+        sz.advance(waves * TS);
+        bc.sb.advance(waves * TS);
+        bc.sc.advance(waves * TS);
     };
-    fetch(k.t0 + wave * TS);
+    fetch(k.t1 - start);
     int buf = 0;
     for (int t0 = k.t0; t0 < k.t1; t0 += waves * TS, buf ^= 1) {
         const int t = t0 + wave * TS, rem = k.t1 - t;  // rem may be below 1: then no token is valid
@@ -135,7 +141,7 @@ __global__ __launch_bounds__(waves * 64, 2) void scan_kernel(ScanArgs a)
             zv[i] = LOCAL ? 0.0f : E::to(z[i]);
         }
         bc.store(lb, lc, !LOCAL);
-        fetch(t + waves * TS);
+        fetch(rem - waves * TS);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
         run_delta = quad_sum(run_delta);
@@ -193,7 +199,8 @@ __global__ __launch_bounds__(waves * 64, 2) void scan_kernel(ScanArgs a)
             continue;
         }
         // and the run from it
-        const auto by = rows_of<E>(a.y, (long long)t * a.d, rem < TS ? rem : TS, a.d, a.d);
+        const auto by = sy.rows(rem < TS ? rem : TS);
+        sy.advance(waves * TS);
 #pragma unroll
         for (int i = 0; i < G; ++i) {
             const Four<NL> C = ahead;
@@ -262,20 +269,39 @@ __global__ __launch_bounds__(256) void scan_join_kernel(ScanArgs a)
     if (i >= per) return;
     const long long ch = i / a.n;
     const float A2 = a.A[i] * kLog2e;
+    // Eight chunks' values are loaded together: one after the other, each would
+    // wait for memory.
+    constexpr int AHEAD = 8;
+    float own[AHEAD], decay[AHEAD];
+    auto fetch = [&](const float *from, int c0, int dir) {
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) {
+            const int c = c0 + dir * u;
+            if (c < 0 || c >= count) continue;
+            own[u] = from[(first + c) * per + i];
+            decay[u] = a.chunk_delta[(long long)(first + c) * a.d + ch];
+        }
+    };
     float h = a.initial ? a.initial[s * per + i] : 0.0f;
-    for (int c = 0; c < count; ++c) {
-        float *p = a.chunk_state + (first + c) * per + i;
-        const float own = *p;
-        *p = h;
-        if (c + 1 < count) h = __builtin_fmaf(__builtin_amdgcn_exp2f(A2 * a.chunk_delta[(long long)(first + c) * a.d + ch]), h, own);
+    for (int c0 = 0; c0 < count; c0 += AHEAD) {
+        fetch(a.chunk_state, c0, 1);
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) {
+            if (c0 + u >= count) break;
+            a.chunk_state[(first + c0 + u) * per + i] = h;
+            h = __builtin_fmaf(__builtin_amdgcn_exp2f(A2 * decay[u]), h, own[u]);  // after the last chunk not used
+        }
     }
     if (!a.chunk_back) return;
     float b = a.dfinal ? a.dfinal[s * per + i] : 0.0f;
-    for (int c = count - 1; c >= 0; --c) {
-        float *p = a.chunk_back + (first + c) * per + i;
-        const float own = *p;
-        *p = b;
-        b = __builtin_fmaf(__builtin_amdgcn_exp2f(A2 * a.chunk_delta[(long long)(first + c) * a.d + ch]), b, own);
+    for (int c0 = count - 1; c0 >= 0; c0 -= AHEAD) {
+        fetch(a.chunk_back, c0, -1);
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) {
+            if (c0 - u < 0) break;
+            a.chunk_back[(first + c0 - u) * per + i] = b;
+            b = __builtin_fmaf(__builtin_amdgcn_exp2f(A2 * decay[u]), b, own[u]);
+        }
     }
     if (a.dinitial) a.dinitial[s * per + i] = b;
 }

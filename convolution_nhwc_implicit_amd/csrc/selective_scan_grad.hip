@@ -28,24 +28,23 @@ void launch_scan_join(const ScanArgs &a, hipStream_t st);
 
 namespace {
 
-// What a step's tokens read, as stored.
+// What a step's tokens read, as stored, from row t on.
 template <class E, int TS>
 struct Tokens {
     static constexpr int G = TS / 4;
     typename E::S x[G], dt[G], z[G], dy[G];
     TokenAt<E> ax, adt, az, ady;
-    __device__ inline Tokens(const ScanArgs &a, const Channels &c)
-        : ax(c, a.xs.row), adt(c, a.dts.row), az(c, a.z ? a.zs.row : 0), ady(c, a.dys.row)
+    Stream<E> sx, sdt, sz, sdy;
+    __device__ inline Tokens(const ScanArgs &a, const Channels &c, const Chunk &k, int t)
+        : ax(c, a.xs.row), adt(c, a.dts.row), az(c, a.z ? a.zs.row : 0), ady(c, a.dys.row),
+          sx(a.x, a.xs.at(a.q, k.s, t), a.xs.row, a.d), sdt(a.dt, a.dts.at(a.q, k.s, t), a.dts.row, a.d),
+          sz(a.z, a.zs.at(a.q, k.s, t), a.zs.row, a.d), sdy(a.dy, a.dys.at(a.q, k.s, t), a.dys.row, a.d)
     {
     }
     // without z its rows read as zero
-    __device__ inline void fetch(const ScanArgs &a, const Chunk &k, int t, bool grad)
+    __device__ inline void fetch(int rows, bool grad)
     {
-        const int rows = k.t1 - t < TS ? k.t1 - t : TS;
-        const auto bx = rows_of<E>(a.x, a.xs.at(a.q, k.s, t), rows, a.xs.row, a.d);
-        const auto bdt = rows_of<E>(a.dt, a.dts.at(a.q, k.s, t), rows, a.dts.row, a.d);
-        const auto bdy = rows_of<E>(a.dy, a.dys.at(a.q, k.s, t), rows, a.dys.row, a.d);
-        const auto bz = rows_of<E>(a.z, a.z ? a.zs.at(a.q, k.s, t) : 0, a.z ? rows : 0, a.zs.row, a.d);
+        const auto bx = sx.rows(rows), bdt = sdt.rows(rows), bdy = sdy.rows(rows), bz = sz.rows(rows);
 #pragma unroll
         for (int i = 0; i < G; ++i) {
             x[i] = get<E>(bx, ax[i]);
@@ -53,6 +52,13 @@ struct Tokens {
             if (grad) dy[i] = get<E>(bdy, ady[i]);
             if (grad) z[i] = get<E>(bz, az[i]);
         }
+    }
+    __device__ inline void advance(int n)
+    {
+        sx.advance(n);
+        sdt.advance(n);
+        sz.advance(n);
+        sdy.advance(n);
     }
 };
 
@@ -79,19 +85,27 @@ __global__ __launch_bounds__(256) void scan_keep_kernel(ScanArgs a)
     float sum_delta = 0.0f;
 
     __shared__ float lb[2][TS * 4 * NL], lc[2][TS * 4 * NL];
-    Tokens<E, TS> in(a, c);
-    StageBC<E, NL, TS> bc(a);
-    if (k.t0 < k.t1) {
-        in.fetch(a, k, k.t0, CARRY);
-        bc.load(a, k, c.group, k.t0, CARRY);
-    }
+    Tokens<E, TS> in(a, c, k, k.t0);
+    StageBC<E, NL, TS> bc(a, k, c.group, k.t0);
+    auto fetch = [&](int rem) {
+        const int rows = rem < TS ? rem : TS;
+        in.fetch(rows, CARRY);
+        bc.load(rows, CARRY);
+        in.advance(TS);
+        bc.advance(TS);
+    };
+    fetch(k.t1 - k.t0);
+    const long long keep = scan_keep_index<TS>(k, slot, k.t0);
+    float *check = a.check + keep * a.d * a.n, *check_delta = a.check_delta + keep * a.d;
     int buf = 0;
-    for (int t = k.t0; t < k.t1; t += TS, buf ^= 1) {
-        const int rem = k.t1 - t;
-        const long long keep = scan_keep_index<TS>(k, slot, t);
+    for (int rem = k.t1 - k.t0; rem > 0; rem -= TS, buf ^= 1) {
         float delta[G], dx[G], g[G], step_delta = 0.0f;
-        at.store(a.check, keep, h);
-        if (CARRY) channel_store(a.check_delta, keep, a, c, sum_delta);
+        at.store(check, 0, h);
+        check += (long long)a.d * a.n;
+        if (CARRY) {
+            channel_store(check_delta, 0, a, c, sum_delta);
+            check_delta += a.d;
+        }
 #pragma unroll
         for (int i = 0; i < G; ++i) {
             const bool valid = c.valid && 4 * i + part < rem;
@@ -109,10 +123,7 @@ __global__ __launch_bounds__(256) void scan_keep_kernel(ScanArgs a)
         }
         if (CARRY) sum_delta += quad_sum(step_delta);
         bc.store(lb[buf], CARRY ? lc[buf] : nullptr);
-        if (rem > TS) {
-            in.fetch(a, k, t + TS, CARRY);
-            bc.load(a, k, c.group, t + TS, CARRY);
-        }
+        fetch(rem - TS);
         __syncthreads();
         Four<NL> nb, nc;
         nb.read(lb[buf], 0, part);
@@ -180,24 +191,30 @@ __global__ __launch_bounds__(256, NL > 8 ? 1 : 2) void scan_back_kernel(ScanArgs
 
     __shared__ float lb[TS * N4], lc[TS * N4];
     __shared__ float sb[4][TS * N4], sc[4][TS * N4];  // the waves' sums of dB and dC
-    Tokens<E, TS> in(a, c);
-    StageBC<E, NL, TS> bc(a);
+    const int len = k.t1 - k.t0, last = k.t0 + (len > 0 ? (len - 1) / TS * TS : 0);  // the last step, perhaps short
+    Tokens<E, TS> in(a, c, k, last);
+    StageBC<E, NL, TS> bc(a, k, c.group, last);
     const TokenAt<E> ao(c, a.d);
+    // where the step's rows lie in du, ddt and dz, and in part_B and part_C
+    long long out = (long long)last * a.d * E::kBytes, part_out = ((long long)c.block * a.q.tokens + last) * a.n * 4;
     // this thread's value of a step's dB and dC
     const uint32_t sum_off = tid < TS * N4 && tid % N4 < a.n ? (uint32_t)(tid / N4 * a.n + tid % N4) * 4 : kNowhere;
+    const long long keep = scan_keep_index<TS>(k, slot, last);
+    const float *check = a.check + keep * a.d * a.n, *check_delta = a.check_delta + keep * a.d;
     float kept[NL], kept_delta = 0.0f;
-    auto fetch = [&](int t) {
-        in.fetch(a, k, t, true);
-        bc.load(a, k, c.group, t, true);
-        const long long keep = scan_keep_index<TS>(k, slot, t);
-        at.load(a.check, keep, kept);
-        if (joined) kept_delta = channel_load(a.check_delta, keep, a, c);
+    auto fetch = [&](int rows) {
+        in.fetch(rows, true);
+        bc.load(rows, true);
+        at.load(check, 0, kept);
+        if (joined) kept_delta = channel_load(check_delta, 0, a, c);
+        in.advance(-TS);
+        bc.advance(-TS);
+        check -= (long long)a.d * a.n;
+        check_delta -= a.d;
     };
-    const int len = k.t1 - k.t0;
-    int t = k.t0 + (len - 1) / TS * TS;  // the last step, perhaps short
-    if (len > 0) fetch(t);
-    for (int left = (len + TS - 1) / TS; left > 0; --left, t -= TS) {
-        const int rem = k.t1 - t < TS ? k.t1 - t : TS;
+    if (len > 0) fetch(k.t1 - last);
+    int rem = k.t1 - last;
+    for (int left = (len + TS - 1) / TS; left > 0; --left, rem = TS) {
         float delta[G], dx[G], xv[G], g[G], dyv[G], zv[G], sig_raw[G], h0[NL];
 #pragma unroll
         for (int i = 0; i < G; ++i) {
@@ -222,7 +239,7 @@ __global__ __launch_bounds__(256, NL > 8 ? 1 : 2) void scan_back_kernel(ScanArgs
             if (joined) h0[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(kept_delta * (A[j] * kLog2e)), H0[j], h0[j]);
         }
         bc.store(lb, lc);
-        if (left > 1) fetch(t - TS);
+        if (left > 1) fetch(TS);
         __syncthreads();
 
         float e[TS][NL], h[TS][NL], ys[G];
@@ -259,9 +276,10 @@ __global__ __launch_bounds__(256, NL > 8 ? 1 : 2) void scan_back_kernel(ScanArgs
             ys[i] = quad_scatter_sum(acc[0], acc[1], acc[2], acc[3], odd, high);
             __builtin_amdgcn_sched_barrier(0);
         }
-        const auto bdu = rows_of<E>(a.du, (long long)t * a.d, rem, a.d, a.d);
-        const auto bdz = rows_of<E>(a.dz, (long long)t * a.d, a.z ? rem : 0, a.d, a.d);  // without z nothing is written
-        const auto bddt = rows_of<E>(a.ddt, (long long)t * a.d, rem, a.d, a.d);
+        const uint32_t out_bytes = (uint32_t)(rem * a.d) * E::kBytes;
+        const auto bdu = buffer_of((char *)a.du + out, out_bytes), bddt = buffer_of((char *)a.ddt + out, out_bytes);
+        const auto bdz = buffer_of((char *)a.dz + out, a.z ? out_bytes : 0);  // without z nothing is written
+        out -= (long long)TS * a.d * E::kBytes;
 #pragma unroll
         for (int i = G - 1; i >= 0; --i) {
             const Four<NL> B = nb, C = nc;  // of group i: the last group's are still there
@@ -312,12 +330,11 @@ __global__ __launch_bounds__(256, NL > 8 ? 1 : 2) void scan_back_kernel(ScanArgs
         }
         __syncthreads();
         if (tid < TS * N4) {
-            const long long o = ((long long)c.block * a.q.tokens + t) * a.n;
-            put<SF32>(buffer_of(a.part_B + o, (uint32_t)(rem * a.n) * 4), sum_off,
-                      (sb[0][tid] + sb[1][tid]) + (sb[2][tid] + sb[3][tid]));
-            put<SF32>(buffer_of(a.part_C + o, (uint32_t)(rem * a.n) * 4), sum_off,
-                      (sc[0][tid] + sc[1][tid]) + (sc[2][tid] + sc[3][tid]));
+            const uint32_t bytes = (uint32_t)(rem * a.n) * 4;
+            put<SF32>(buffer_of((char *)a.part_B + part_out, bytes), sum_off, (sb[0][tid] + sb[1][tid]) + (sb[2][tid] + sb[3][tid]));
+            put<SF32>(buffer_of((char *)a.part_C + part_out, bytes), sum_off, (sc[0][tid] + sc[1][tid]) + (sc[2][tid] + sc[3][tid]));
         }
+        part_out -= (long long)TS * a.n * 4;
     }
     // a slot that no chunk uses adds nothing
     at.store(a.part_A, slot, dA);
@@ -339,6 +356,7 @@ __global__ __launch_bounds__(256) void scan_sum_kernel(ScanArgs a, unsigned bc_b
         const long long t = i / ((long long)a.n * a.groups);
         float b = 0.0f, c = 0.0f;
         const long long o = (long long)grp * a.blocks_per_group * per + t * a.n + n;
+#pragma unroll 8
         for (int k = 0; k < a.blocks_per_group; ++k) {
             b += a.part_B[o + k * per];
             c += a.part_C[o + k * per];
@@ -366,6 +384,7 @@ __global__ __launch_bounds__(256) void scan_sum_kernel(ScanArgs a, unsigned bc_b
     }
     if (i >= per || !out) return;
     float v = 0.0f;
+#pragma unroll 8
     for (int s = 0; s < a.slots; ++s) v += p[s * per + i];
     out[i] = v;
 }
