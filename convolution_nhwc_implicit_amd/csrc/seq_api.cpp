@@ -120,28 +120,72 @@ struct ScanPlan {
     size_t state, delta, check, check_delta, part_B;  // bytes
 };
 
-// Tokens per chunk.  Forward: a sequence's workgroups (16 channels, up to 8
-// waves) walk it whole where they give the chip a wave per SIMD; below that
-// chunks, though walked twice, take less time.  Gradient (64 channels, 4 waves):
-// two workgroups to a compute unit.
+// How many waves of a forward workgroup take runs of a walk of `len` tokens: as
+// many as it has runs, and no more than give each SIMD two waves.
+int scan_waves(long long walks, long long len, int ts)
+{
+    int w = 8;
+    while (w > 1 && (w / 2 * ts >= len || walks * (w / 2) >= 2 * 4 * kCUs)) w /= 2;
+    return w;
+}
+
+// Microseconds of a forward pass with sequences cut into chunks of `chunk` tokens
+// (walked twice and joined) or, if longest <= chunk, not cut.  A segment (waves *
+// ts tokens) was measured at 2.8 us where workgroups have the compute units to
+// themselves, 3.7 us at two waves per SIMD; chunks add a shorter first walk,
+// launches, and the join's batches of eight.
+double scan_time(double blocks, const seq_batch_t &b, long long longest, long long chunk, int ts, double weight)
+{
+    const bool cut = longest > chunk;
+    const double pieces = cut ? (double)b.tokens / chunk + (b.seq_start ? 0.5 * b.seqs : 0) : b.seqs, walks = blocks * pieces;
+    const long long len = cut ? chunk : longest;
+    const int w = scan_waves((long long)walks, len, ts);
+    const double segment = weight * (walks * w > 4 * kCUs ? 3.7 : 2.8), slots = 2.0 * 4 * kCUs / w;
+    const double alone = (double)ceil_div(len, (long long)w * ts), all = (double)b.tokens / (w * ts) * blocks / slots;
+    const double walk = std::max(alone, all) * segment;
+    return cut ? 1.65 * walk + 10 + 0.8 * (double)ceil_div(ceil_div(longest, chunk), 8) : walk;
+}
+
+// The same for the gradient: a step of ts tokens of both walks 3.9 us for up to a
+// workgroup to a compute unit, 6.6 us for two, in rounds.
+double scan_grad_time(double blocks, const seq_batch_t &b, long long longest, long long chunk, int ts, double weight)
+{
+    const bool cut = longest > chunk;
+    const double pieces = cut ? (double)b.tokens / chunk + (b.seq_start ? 0.5 * b.seqs : 0) : b.seqs;
+    const long long walks = std::max(1LL, (long long)(blocks * pieces)), rest = walks % (2 * kCUs);
+    const double round = (double)(walks / (2 * kCUs)) * 6.6 + (rest == 0 ? 0 : rest <= kCUs ? 3.9 : 6.6);
+    return (double)ceil_div(std::min(longest, chunk), ts) * round * weight +
+           (cut ? 5 + 1.6 * (double)ceil_div(ceil_div(longest, chunk), 8) : 0);
+}
+
+// Tokens per chunk: what the estimates above say takes least time.  The lengths
+// of packed sequences are on the device: the longest is taken as twice the mean.
 void scan_plan(const selective_scan_problem_t *p, bool grad, ScanPlan *s)
 {
     const seq_batch_t &b = p->batch;
     const int ts = grad ? scan_grad_step_tokens(p->n) : scan_step_tokens(p->n);
+    const int nl = p->n <= 4 ? 1 : p->n <= 8 ? 2 : p->n <= 16 ? 4 : p->n <= 32 ? 8 : 16;
+    const double weight = std::max(0.6, (double)nl * ts / (grad ? 32 : 64));
     s->blocks_per_group = (int)ceil_div(p->d / p->groups, grad ? kScanChannels : kScanWaveChannels);
-    const long long blocks = (long long)s->blocks_per_group * p->groups, walks = blocks * b.seqs;
-    const long long longest = b.seq_start ? b.tokens : b.len;
-    long long chunk = std::max<long long>(ceil_div(longest, 16) * 16, 16);
-    s->waves = 8;
-    while (s->waves > 1 && (s->waves / 2 * ts >= longest || walks * (s->waves / 2) >= 2 * 4 * kCUs)) s->waves /= 2;
-    const long long want = grad ? 2 * kCUs : 2 * 4 * kCUs / s->waves;
-    if (grad ? walks < want : 2 * walks < want) {
-        const long long pieces = std::max<long long>(1, want / blocks), least = grad ? 64 : s->waves * ts;
-        chunk = std::min(chunk, std::max<long long>(least, ceil_div(ceil_div(b.tokens, pieces), 16) * 16));
+    const long long blocks = (long long)s->blocks_per_group * p->groups;
+    const long long whole = std::max<long long>(ceil_div(b.seq_start ? b.tokens : b.len, 16) * 16, 16);
+    const long long longest = b.seq_start ? std::max(1LL, std::min(b.tokens, 2 * ceil_div(b.tokens, b.seqs))) : std::max(1, b.len);
+    auto time = [&](long long c) {
+        return grad ? scan_grad_time((double)blocks, b, longest, c, ts, weight) : scan_time((double)blocks, b, longest, c, ts, weight);
+    };
+    long long chunk = whole;
+    double best = time(whole);
+    for (long long c = grad ? 16 : 4 * ts; c < whole; c += std::max<long long>(16, c / 4 / 16 * 16)) {
+        const double t = time(c);
+        if (t < best && b.tokens / c + b.seqs < (1 << 24)) {
+            best = t;
+            chunk = c;
+        }
     }
     s->chunk = (int)std::min<long long>(chunk, 1 << 30);
+    s->waves = scan_waves(blocks * (longest > chunk ? b.tokens / chunk + 1 : b.seqs), std::min(longest, chunk), ts);
     s->chunks = std::max(1, (int)ceil_div(b.len, s->chunk));
-    s->joined = longest > s->chunk;
+    s->joined = whole > s->chunk;
     s->slots = b.seq_start ? (int)(b.tokens / s->chunk) + b.seqs : s->chunks * b.seqs;
     const size_t dn = (size_t)p->d * p->n * 4, d = (size_t)p->d * 4;
     s->state = up(s->slots * dn);
