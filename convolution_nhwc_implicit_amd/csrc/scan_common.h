@@ -144,7 +144,7 @@ __device__ inline Chunk find_chunk(const ScanArgs &a, int slot)
     r.last = c == count - 1;
     const long long b = a.q.begin(r.s), e = a.q.end(r.s);
     long long t0 = b + (long long)c * a.chunk;
-    if (t0 > e) t0 = e;
+    t0 = t0 < b ? b : t0 > e ? e : t0;  // inside whatever seq_start says
     const long long t1 = t0 + a.chunk < e ? t0 + a.chunk : e;
     r.t0 = uniform((int)t0);
     r.t1 = found ? uniform((int)t1) : r.t0;
