@@ -450,11 +450,13 @@ __global__ __launch_bounds__(256) void fp8_sum_kernel(const float *part, int spl
     store_out4<E>(out, i, have, v);
 }
 
-// Products with few rows on one side ("small", at most 64) stream the other
-// side's rows ("big") once: bound by its bytes.  A workgroup owns 16 big rows and
-// its waves share the blocks of k, four (or two) of a wave's on their way at a time,
+// Products with few rows on one side ("small") stream the other side's rows
+// ("big"): bound by its bytes.  A workgroup owns 16 big rows and up to 64 small
+// ones (blockIdx.y), and its waves share the blocks of k, four (or two) of a wave's on their way at a time,
 // straight to registers; their sums are added in order through LDS.  Scales are
 // applied to each block's sum in fp32: there is time for it.
+constexpr int kNarrow = 64;
+
 struct NarrowArgs {
     const uint8_t *big, *small;
     const float *big_scale, *small_scale;
@@ -475,6 +477,7 @@ __global__ __launch_bounds__(512) void fp8_narrow_kernel(NarrowArgs a)
     const int each_wave = (a.kb + waves - 1) / waves;
     const int kb0 = wave * each_wave, kb1 = kb0 + each_wave < a.kb ? kb0 + each_wave : a.kb;
     const long long b0 = (long long)blockIdx.x * 16;
+    const int s0 = blockIdx.y * kNarrow, small_rows = a.small_rows - s0 < kNarrow ? a.small_rows - s0 : kNarrow;
     // rows past the matrix are its last row again; what they give is not written
     const long long brow = b0 + lr < a.big_rows ? b0 + lr : a.big_rows - 1;
     const uint8_t *pb = a.big + brow * a.big_pitch + quarter * 16;
@@ -483,7 +486,7 @@ __global__ __launch_bounds__(512) void fp8_narrow_kernel(NarrowArgs a)
     const float *ss[MT];
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
-        const long long r = i * 16 + lr < a.small_rows ? i * 16 + lr : a.small_rows - 1;
+        const long long r = s0 + (i * 16 + lr < small_rows ? i * 16 + lr : small_rows - 1);
         ps[i] = a.small + r * a.small_pitch + quarter * 16;
         ss[i] = a.small_scale + (a.small_blocks ? (a.small_first + r) / kFp8Block : a.small_first + r) * a.kb;
     }
@@ -577,8 +580,8 @@ __global__ __launch_bounds__(512) void fp8_narrow_kernel(NarrowArgs a)
         }
         const int s = t / 64 * 16 + t % 16;
         const long long b = b0 + t % 64 / 16 * 4;
-        if (s >= a.small_rows) continue;
-        typename E::S *o = (typename E::S *)a.out + s * a.small_step;
+        if (s >= small_rows) continue;
+        typename E::S *o = (typename E::S *)a.out + (s0 + s) * a.small_step;
         if (a.big_step == 1 && b + 4 <= a.big_rows) {
             const float r[4] = {v[0], v[1], v[2], v[3]};
             store_vec<E, 4>(o + b, 4, r);
@@ -590,19 +593,24 @@ __global__ __launch_bounds__(512) void fp8_narrow_kernel(NarrowArgs a)
     }
 }
 
-constexpr int kNarrow = 64;
+// Waves along k: where there are so many blocks at least two each, and no more
+// than fill the chip.
+int narrow_waves(long long workgroups, int kb)
+{
+    int waves = 4;
+    if (workgroups * waves < 4096 && kb >= waves * 2) waves = 8;
+    while (waves > 1 && waves > kb) waves /= 2;
+    return waves;
+}
 
 template <class E, class UNIT>
 hipError_t launch_narrow(const NarrowArgs &a, hipStream_t st)
 {
-    // waves along k: at least two batches each where there are so many blocks,
-    // and no more than fill the chip
-    const int groups = (a.big_rows + 15) / 16, mt = (a.small_rows + 15) / 16;
-    int waves = 4;
-    if (groups * waves < 4096 && a.kb >= waves * 4) waves = 8;
+    const int groups = (a.big_rows + 15) / 16, parts = (a.small_rows + kNarrow - 1) / kNarrow;
+    const int mt = parts > 1 ? 4 : (a.small_rows + 15) / 16, waves = narrow_waves((long long)groups * parts, a.kb);
     auto run = [&](auto mtc, auto batch) {
         constexpr int MT = decltype(mtc)::value;
-        fp8_narrow_kernel<E, UNIT, MT, decltype(batch)::value><<<dim3((unsigned)groups), waves * 64, waves * MT * 1024, st>>>(a);
+        fp8_narrow_kernel<E, UNIT, MT, decltype(batch)::value><<<dim3((unsigned)groups, (unsigned)parts), waves * 64, waves * MT * 1024, st>>>(a);
         return hipGetLastError();
     };
     using std::integral_constant;
@@ -642,12 +650,12 @@ double tiles_time(const TileCost &s, double step, long long m, long long n, int 
     // the last round's tiles have the compute units to themselves
     const long long last = tiles * splits - (rounds - 1) * slots;
     const double alone = s.per_cu > 1 && last <= 256 ? 0.65 : 1.0;
-    return ((rounds - 1) + alone) * (per * step + 3.0);
+    return 6.0 + ((rounds - 1) + alone) * (per * step + 3.0);
 }
 
 }  // namespace
 
-// How a product is cut.  Few rows on either side: the narrow kernel.  Else tiles
+// How a product is cut.  Few rows on either side, or little work: the narrow kernel.  Else tiles
 // of the shape that takes least time by the steps above, in whole rounds over the
 // chip; with a few rows past whole tiles on either side left to the narrow kernel
 // where that saves more than its pass over the other operand takes; and with k
@@ -663,7 +671,14 @@ Fp8Plan fp8_matmul_plan(int m, int n, int k, int dtype)
         best.narrow_n = !best.narrow_m;
         return best;
     }
-    double best_t = 1e30;
+    // Small products all through the narrow kernel, which needs no partial sums:
+    // measured 3.5 us, and 1.8 us (float32 results, which convert 80 rows to bf16:
+    // 4.5 us) a block of a wave's, three workgroups to a compute unit at a time.
+    const long long groups = (long long)((n + 15) / 16) * ((m + kNarrow - 1) / kNarrow);
+    const int waves = narrow_waves(groups, kb);
+    double best_t = std::max(1.0, groups / 768.0) * (3.5 + (dtype == CONV2D_DTYPE_F32 ? 4.5 : 1.8) * ((kb + waves - 1) / waves));
+    if ((m + kNarrow - 1) / kNarrow <= 65535) best.all = best.narrow_m = true;
+    else best_t = 1e30;
     for (int shape = 0; shape < 2; ++shape) {
         const TileCost &s = kTiles[shape];
         const double step = dtype == CONV2D_DTYPE_F32 ? s.step32 : s.step16;
@@ -680,6 +695,7 @@ Fp8Plan fp8_matmul_plan(int m, int n, int k, int dtype)
                 if (split > 1) t += 3.0 + (double)m * n * 4 * (2 * split + 1) / 5e6;
                 if (t < best_t) {
                     best_t = t;
+                    best.all = false;
                     best.shape = shape;
                     best.splits = split;
                     best.per = per;
@@ -720,7 +736,7 @@ static hipError_t launch_tiles(Fp8MatmulArgs a, const Fp8Plan &p, hipStream_t st
 template <class E, class UNIT>
 static hipError_t launch_parts(Fp8MatmulArgs a, const Fp8Plan &p, hipStream_t st)
 {
-    if (p.narrow_m && a.m <= kNarrow) return narrow_rows_of_a<E, UNIT>(a, 0, a.n, st);
+    if (p.all || (p.narrow_m && a.m <= kNarrow)) return narrow_rows_of_a<E, UNIT>(a, 0, a.n, st);
     if (p.narrow_n && a.n <= kNarrow) return narrow_rows_of_b<E, UNIT>(a, 0, st);
     const TileCost &s = kTiles[p.shape];
     const int mm = p.narrow_m ? a.m / s.bm * s.bm : a.m, nn = p.narrow_n ? a.n / s.bn * s.bn : a.n;

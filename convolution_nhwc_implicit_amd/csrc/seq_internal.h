@@ -117,6 +117,7 @@ struct Fp8MatmulArgs {
 struct Fp8Plan {
     int shape, splits, per;  // tile shape; workgroups along k, and blocks of each
     bool narrow_m, narrow_n; // the rows of a, or of b, past whole tiles go to the narrow kernel
+    bool all;                // everything does
 };
 
 hipError_t launch_fp8_quantize(int form, int dtype, const Fp8QuantArgs &a, hipStream_t st);
