@@ -3,7 +3,9 @@
 The computation runs in hand-written HIP kernels behind the C ABI declared in
 include/conv2d_nhwc.h (libconv2d_nhwc.so, built by
 ``python -m convolution_nhwc_implicit_amd.build``).  This package is the thin
-ctypes binding to it; PyTorch provides device memory and streams.
+ctypes binding to it; PyTorch provides device memory and streams.  The sequence
+operators (causal convolution, selective scan, block-scaled fp8 products) are
+bound in sequence.py.
 """
 from .binding import (  # noqa: F401
     CONV2D_DTYPE_BF16, CONV2D_DTYPE_F16, CONV2D_DTYPE_I8, CONV2D_OP_DGRAD, CONV2D_OP_FPROP,

@@ -167,7 +167,7 @@ def test_matmul_empty():
 
 
 def test_linear_and_its_gradients():
-    """A projection from 16-bit activations, and both its gradients, as perf users call them: against the products of
+    """A projection from 16-bit activations, and both its gradients: against the products of
     the values that the quantised operands stand for."""
     g = gen(9)
     m, n, k = 70, 200, 333
