@@ -6,8 +6,8 @@
 // operands' rows go to LDS by direct loads, double buffered, and from there as
 // 16x16x128 matrix instructions' fragments.  b is the instruction's first
 // operand, so that a lane ends up with four neighbouring columns of a row of out.
-// 4057 x 8200 x 4104: 153 us (1.8 PFLOP/s), bound by the blocks' arrival (64 KB in
-// ~1.2 us with one block on its way); the matrix unit alone would take 57.
+// 4057 x 8200 x 4104: 153 us (1.8 PFLOP/s) where the matrix unit is busy for 57; the
+// rest is waiting for blocks (64 KB each, one on its way) and writing results.
 #include <algorithm>
 #include <utility>
 

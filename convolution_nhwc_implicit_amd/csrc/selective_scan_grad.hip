@@ -23,7 +23,7 @@
 //
 // Bound by the vector units at two waves a SIMD: on 4 x 2048 tokens, 2048 channels,
 // 16 states the first walk takes 117 us (1540 of their cycles per 8 tokens of a
-// wave), the backward walk 269 us (3470), the sums 10 us.
+// wave), the backward walk 269 us (3472), the sums 10 us.
 #include "scan_common.h"
 
 namespace cnv {
