@@ -295,12 +295,11 @@ struct Tile {
                 const auto fa = UNIT::template prepare<i % 4>(raw, ea[i / 4]);
                 if (i + 1 < MT) raw = frag_a(buf, i + 1);
                 if (i == MT - 2) {
-                    if (buf == 0) {
-                        put_scales(pair ^ 2, scales);
-                        scales = load_scales(kb + 4);
-                    }
+                    if (buf == 0) put_scales(pair ^ 2, scales);
                     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
                     arrive(kb + 1, buf ^ 1);
+                    // behind the block's loads: before them, arrive would wait for these
+                    if (buf == 0) scales = load_scales(kb + 4);
                     nb = exps_b(slot);
 #pragma unroll
                     for (int q = 0; q < MT / 4; ++q) na[q] = exps_a(slot, q);
