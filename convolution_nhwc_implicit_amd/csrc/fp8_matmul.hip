@@ -640,8 +640,9 @@ struct TileCost {
     int bm, bn, per_cu;
     double step16, step32;  // microseconds per block of 128 for per_cu tiles at a time: 16-bit results, float32
 };
-// Measured on 4096 x 8192 x 4096: 256 x 256 125 us, 128 x 128 137 us (float32
-// results: 220 us; 256 x 256 would spill there).
+// Measured on 4096 x 8192 x 4096, normal data: 256 x 256 138-144 us, 128 x 128 165 us.
+// On constant operands, which take less power: 121 and 140 (float32 results 128 x 128
+// 214-220, 256 x 256 314: it spills); the steps below are from those.
 static const TileCost kTiles[] = {{256, 256, 1, 1.95, 0}, {128, 128, 2, 1.07, 1.7}};
 
 double tiles_time(const TileCost &s, double step, long long m, long long n, int per, int splits)
