@@ -30,7 +30,7 @@ struct WaveBC {
     typename E::S b[kEach], c[kEach];
     uint32_t boff, coff;
     Stream<E> sb, sc;
-    __device__ inline WaveBC(const ScanArgs &a, const Chunk &q, int group, int t)
+    __device__ inline WaveBC(const ScanArgs &a, const Chunk &q, int group, long long t)
         : sb(a.B, a.bs.at(a.q, q.s, t) + group * a.b_group, a.bs.row, a.n),
           sc(a.C, a.cs.at(a.q, q.s, t) + group * a.c_group, a.cs.row, a.n)
     {
@@ -104,9 +104,10 @@ __global__ __launch_bounds__(waves * 64, 2) void scan_kernel(ScanArgs a)
     float *lb = shared + 2 * kEnds + wave * 2 * WaveBC<E, NL, TS>::kEach * 64, *lc = lb + WaveBC<E, NL, TS>::kEach * 64;
 
     const TokenAt<E> ax(c, a.xs.row), adt(c, a.dts.row), az(c, gated ? a.zs.row : 0), ay(c, a.d);
-    const int start = k.t0 + wave * TS;
+    // Rows are counted down from the chunk's length: k.t0 + .. may pass 31 bits behind the last row.
+    const long long start = (long long)k.t0 + wave * TS;
     Stream<E> sx(a.x, a.xs.at(a.q, k.s, start), a.xs.row, a.d), sdt(a.dt, a.dts.at(a.q, k.s, start), a.dts.row, a.d);
-    Stream<E> sz(gated ? a.z : nullptr, a.zs.at(a.q, k.s, start), a.zs.row, a.d), sy(a.y, (long long)start * a.d, a.d, a.d);
+    Stream<E> sz(gated ? a.z : nullptr, a.zs.at(a.q, k.s, start), a.zs.row, a.d), sy(a.y, start * a.d, a.d, a.d);
     S x[G], dt[G], z[G];
     WaveBC<E, NL, TS> bc(a, k, c.group, start);
     // rows past the chunk read as zero, and a whole run past it takes no memory
@@ -126,10 +127,11 @@ __global__ __launch_bounds__(waves * 64, 2) void scan_kernel(ScanArgs a)
         bc.sb.advance(waves * TS);
         bc.sc.advance(waves * TS);
     };
-    fetch(k.t1 - start);
+    const int len = k.t1 - k.t0;
+    fetch(len - wave * TS);
     int buf = 0;
-    for (int t0 = k.t0; t0 < k.t1; t0 += waves * TS, buf ^= 1) {
-        const int t = t0 + wave * TS, rem = k.t1 - t;  // rem may be below 1: then no token is valid
+    for (int left = len; left > 0; left -= waves * TS, buf ^= 1) {
+        const int rem = left - wave * TS;  // may be below 1: then no token is valid
         float delta[G], dx[G], xv[G], zv[G], run_delta = 0.0f;
 #pragma unroll
         for (int i = 0; i < G; ++i) {

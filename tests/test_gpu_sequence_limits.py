@@ -1,0 +1,27 @@
+"""Sequence operators at the ends of their accepted sizes: token numbers up to the last that 31 bits hold."""
+import pytest
+import torch
+
+import convolution_nhwc_implicit_amd as nn
+import sequence_ref as R
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF16 = torch.bfloat16
+
+
+def test_scan_to_the_last_token():
+    """2^31 - 1 tokens of one channel: the loop's count may not pass 31 bits behind the last one.  The end against
+    the 64-bit form from 1000 tokens back, of which exp(-250) would be left."""
+    T, far, cut = 2 ** 31 - 1, 1000, 500
+    g = torch.Generator(device=DEV).manual_seed(3)
+    x = torch.randn(1, T, 1, generator=g, device=DEV, dtype=BF16)
+    one = torch.ones(1, 1, 1, device=DEV, dtype=BF16)
+    dt, BC = (0.5 * one).expand(1, T, 1), one.unsqueeze(-1).expand(1, T, 1, 1)
+    y, final = nn.selective_scan(x, dt, -torch.ones(1, 1, device=DEV), BC, BC, return_state=True)
+    end, out = x[0, T - far:].double().cpu(), y[0, T - cut:].double().cpu()
+    o = torch.ones(far, 1, 1, dtype=torch.float64)
+    want, fin, mag, worst = R.scan(end, 0.5 * o[:, 0], -o[:1, 0], o, o, None, None, None, False, [far])
+    tol = R.half_step(BF16) * want.abs() + R.U * (worst + 24) * mag
+    assert ((out - want[far - cut:]).abs() <= tol[far - cut:]).all()
+    assert abs(float(final) - float(fin)) <= R.U * (worst + 24) * float(mag[-1])
