@@ -96,11 +96,13 @@ struct Chunk {
     bool valid;
 };
 
+// No more than there are in all (fewer than 2^25), which a sequence exceeds only
+// if seq_start descends somewhere: sums over 64 sequences stay within 31 bits.
 __device__ inline int chunks_of(const ScanArgs &a, int s)
 {
     const long long len = a.q.end(s) - a.q.begin(s);
     const long long c = (len + a.chunk - 1) / a.chunk;
-    return c < 1 ? 1 : (int)c;  // an empty sequence still passes its state on
+    return c < 1 ? 1 : c < a.slots ? (int)c : a.slots;  // an empty sequence still passes its state on
 }
 
 // Slot -> chunk.  Packed: sequences' chunks lie in order, 64 sequences looked

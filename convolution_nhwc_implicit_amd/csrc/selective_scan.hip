@@ -263,7 +263,7 @@ __global__ __launch_bounds__(256) void scan_join_kernel(ScanArgs a)
         for (int s0 = 0; s0 < s; s0 += 64) {
             int v = s0 + lane < s ? chunks_of(a, s0 + lane) : 0;
             for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
-            first += v;
+            first = first + v < a.slots ? first + v : a.slots;
         }
         first = __builtin_amdgcn_readfirstlane(first);
         count = chunks_of(a, s);

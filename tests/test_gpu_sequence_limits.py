@@ -25,3 +25,23 @@ def test_scan_to_the_last_token():
     tol = R.half_step(BF16) * want.abs() + R.U * (worst + 24) * mag
     assert ((out - want[far - cut:]).abs() <= tol[far - cut:]).all()
     assert abs(float(final) - float(fin)) <= R.U * (worst + 24) * float(mag[-1])
+
+
+def test_descending_starts_stay_in_bounds():
+    """Starts that go up and down between 0 and 2^20 in 2^15 sequences: their chunks, counted together, pass 31 bits.
+    What they give is not specified, but they may reach nothing outside the buffers, so a batch after them is right."""
+    T, seqs, d = 2 ** 20, 2 ** 15, 1
+    g = torch.Generator(device=DEV).manual_seed(4)
+    x, dt = torch.randn(T, d, generator=g, device=DEV), torch.rand(T, d, generator=g, device=DEV)
+    B, C = (torch.randn(T, 1, 1, generator=g, device=DEV) for _ in range(2))
+    A = -torch.ones(d, 1, device=DEV)
+    rising = torch.arange(seqs + 1, device=DEV, dtype=torch.int32) * (T // seqs)
+    descending = (torch.arange(seqs + 1, device=DEV) % 2 * T).to(torch.int32)
+
+    def run(start):
+        return [v for v in nn.selective_scan_grad(x, x, dt, A, B, C, seq_start=start).values() if v is not None]
+
+    want = run(rising)
+    run(descending)
+    torch.cuda.synchronize()
+    assert all(torch.equal(u, v) for u, v in zip(want, run(rising)))
