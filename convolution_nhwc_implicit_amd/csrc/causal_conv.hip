@@ -425,11 +425,13 @@ hipError_t launch_conv_grad(int dtype, int w, const ConvArgs &a, dim3 grid, hipS
     return by_type(dtype, w, [&](auto e, auto wc) {
         using E = decltype(e);
         constexpr int W = decltype(wc)::value;
-        hipError_t r = by_width(a, [&](auto v, auto wide) {
-            conv_grad_kernel<E, W, decltype(v)::value, decltype(wide)::value><<<grid, 256, 0, st>>>(a);
-            return hipGetLastError();
-        });
-        if (r != hipSuccess) return r;
+        if (grid.x) {  // without rows and states only the sums remain: zeros
+            const hipError_t r = by_width(a, [&](auto v, auto wide) {
+                conv_grad_kernel<E, W, decltype(v)::value, decltype(wide)::value><<<grid, 256, 0, st>>>(a);
+                return hipGetLastError();
+            });
+            if (r != hipSuccess) return r;
+        }
         const long long total = (long long)(W + 1) * a.d;
         conv_sum_kernel<E, W><<<dim3((unsigned)((total + 15) / 16)), 256, 0, st>>>(a.partial, a.run_blocks, a.d,
                                                                                  a.dweight, a.dbias);
