@@ -637,13 +637,13 @@ hipError_t narrow_rows_of_b(const Fp8MatmulArgs &a, int first, hipStream_t st)
 }
 
 struct TileCost {
-    int bm, bn, per_cu;
+    int bm, bn, threads, per_cu;
     double step16, step32;  // microseconds per block of 128 for per_cu tiles at a time: 16-bit results, float32
 };
 // Measured on 4096 x 8192 x 4096, normal data: 256 x 256 138-144 us, 128 x 128 165 us.
 // On constant operands, which take less power: 121 and 140 (float32 results 128 x 128
 // 214-220, 256 x 256 314: it spills); the steps below are from those.
-static const TileCost kTiles[] = {{256, 256, 1, 1.95, 0}, {128, 128, 2, 1.07, 1.7}};
+static constexpr TileCost kTiles[] = {{256, 256, 512, 1, 1.95, 0}, {128, 128, 256, 2, 1.07, 1.7}};
 
 double tiles_time(const TileCost &s, double step, long long m, long long n, int per, int splits)
 {
@@ -676,10 +676,10 @@ Fp8Plan fp8_matmul_plan(int m, int n, int k, int dtype)
     // Small products all through the narrow kernel, which needs no partial sums:
     // measured 3.5 us, and 1.8 us (float32 results, which convert 80 rows to bf16:
     // 4.5 us) a block of a wave's, three workgroups to a compute unit at a time.
-    const long long groups = (long long)((n + 15) / 16) * ((m + kNarrow - 1) / kNarrow);
+    const long long groups = (n + 15LL) / 16 * ((m + kNarrow - 1LL) / kNarrow);
     const int waves = narrow_waves(groups, kb);
     double best_t = std::max(1.0, groups / 768.0) * (3.5 + (dtype == CONV2D_DTYPE_F32 ? 4.5 : 1.8) * ((kb + waves - 1) / waves));
-    if ((m + kNarrow - 1) / kNarrow <= 65535) best.all = best.narrow_m = true;
+    if ((m + kNarrow - 1LL) / kNarrow <= 65535) best.all = best.narrow_m = true;
     else best_t = 1e30;
     for (int shape = 0; shape < 2; ++shape) {
         const TileCost &s = kTiles[shape];
@@ -710,6 +710,21 @@ Fp8Plan fp8_matmul_plan(int m, int n, int k, int dtype)
     return best;
 }
 
+bool fp8_matmul_fits(int m, int n, int k, const Fp8Plan &p)
+{
+    auto narrow = [&](long long big, long long small) {
+        const long long groups = (big + 15) / 16, parts = (small + kNarrow - 1) / kNarrow;
+        return parts <= 65535 && fits(groups, narrow_waves(groups * parts, (k + kFp8Block - 1) / kFp8Block) * 64);
+    };
+    if (p.all || (p.narrow_m && m <= kNarrow)) return narrow(n, m);
+    if (p.narrow_n && n <= kNarrow) return narrow(m, n);
+    const TileCost &s = kTiles[p.shape];
+    const long long rm = p.narrow_m ? m % s.bm : 0, rn = p.narrow_n ? n % s.bn : 0;
+    const long long tiles = (m - rm + s.bm - 1) / s.bm * ((n - rn + s.bn - 1) / s.bn);
+    return fits(tiles, s.threads) && (p.splits == 1 || fits(((long long)m * n + 1023) / 1024, 256)) &&
+           (!rm || narrow(n - rn, rm)) && (!rn || narrow(m, rn));
+}
+
 size_t fp8_matmul_bytes(int m, int n, const Fp8Plan &p) { return p.splits > 1 ? (size_t)p.splits * m * n * 4 : 0; }
 
 template <class E, class UNIT>
@@ -720,6 +735,7 @@ static hipError_t launch_tiles(Fp8MatmulArgs a, const Fp8Plan &p, hipStream_t st
         a.tiles_m = (a.m + BM - 1) / BM;
         a.tiles_n = (a.n + BN - 1) / BN;
         constexpr int lds = Tile<E, UNIT, BM, BN, WM, WN>::kLds;
+        static_assert(kTiles[BM == 256 ? 0 : 1].bm == BM && kTiles[BM == 256 ? 0 : 1].threads == WM * WN * 64, "as fp8_matmul_fits counts");
         auto *kernel = fp8_tile_kernel<E, UNIT, BM, BN, WM, WN>;
         hipError_t r = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
         if (r != hipSuccess) return r;

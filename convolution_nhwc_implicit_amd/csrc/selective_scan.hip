@@ -412,7 +412,7 @@ hipError_t launch_scan_step(int dtype, const ScanStepArgs &a, hipStream_t st)
     const int blocks = (a.d + 63) / 64;
     return scan_by_type(dtype, a.n, [&](auto e, auto nl) {
         using E = decltype(e);
-        constexpr int NL = decltype(nl)::value, R = NL > 4 ? 2 : 4;
+        constexpr int NL = decltype(nl)::value, R = scan_step_rows(4 * NL);
         // few rows: one each, over as many compute units
         if ((long long)a.rows * blocks < 4096) scan_step_kernel<E, NL, 1><<<dim3((unsigned)a.rows, (unsigned)blocks), 256, 0, st>>>(a);
         else scan_step_kernel<E, NL, R><<<dim3((unsigned)((a.rows + R - 1) / R), (unsigned)blocks), 256, 0, st>>>(a);

@@ -80,6 +80,11 @@ ConvPlan conv_plan(const causal_conv_problem_t *p, int v, int most, bool states)
 }
 constexpr int kConvMostRows = 32, kConvGradMostRows = 64;
 
+bool conv_fits(const ConvPlan &c, int d, int v)
+{
+    return ceil_div(d, c.lanes * v) <= kMaxGridY && fits((long long)c.run_blocks + c.state_blocks, 256);
+}
+
 int conv_grad_plan(const causal_conv_problem_t *p, int dtype, bool states, ConvPlan *c, size_t *ws)
 {
     *c = conv_plan(p, conv_channels(p->d), kConvGradMostRows, states);
@@ -199,6 +204,16 @@ void scan_plan(const selective_scan_problem_t *p, bool grad, ScanPlan *s)
     }
 }
 
+// Whether the launches of a pass fit, and the sums of their counts 31 bits.
+bool scan_fits(const selective_scan_problem_t *p, const ScanPlan &s, bool grad)
+{
+    if (s.joined && !fits(p->batch.seqs, 256)) return false;
+    if (!grad) return fits(ceil_div((long long)s.slots * s.blocks_per_group * p->groups, 8) * 8, s.waves * 64);
+    const long long tokens = p->batch.tokens, bc = (long long)p->groups * p->n;  // scan_sum_kernel, a thread to a value
+    return fits(s.slots, 256) && tokens <= kMaxThreads / bc &&
+           fits(ceil_div(tokens * bc, 256) + ceil_div((long long)p->d * (p->n + 2), 256), 256);
+}
+
 size_t scan_bytes(const ScanPlan &s, bool grad)
 {
     if (!grad) return s.joined ? s.state + s.delta : 0;
@@ -252,7 +267,7 @@ int causal_conv(const causal_conv_problem_t *prob, int dtype, const void *x, con
     if (!all_aligned(bytes_of(dtype), {x, weight, bias, initial_state, y, final_state})) return CONV2D_ERR_UNSUPPORTED;
     const int v = conv_channels(prob->d);
     const ConvPlan c = conv_plan(prob, v, kConvMostRows, final_state != nullptr);
-    if (ceil_div(prob->d, c.lanes * v) > kMaxGridY) return CONV2D_ERR_UNSUPPORTED;
+    if (!conv_fits(c, prob->d, v)) return CONV2D_ERR_UNSUPPORTED;
     if (c.run_blocks + c.state_blocks == 0) return CONV2D_OK;
     ConvArgs a = {};
     a.q = seqs_of(prob->batch);
@@ -298,7 +313,7 @@ int causal_conv_grad(const causal_conv_problem_t *prob, int dtype, const void *d
     size_t need;
     conv_grad_plan(prob, dtype, dinitial != nullptr, &c, &need);
     const int v = conv_channels(prob->d);
-    if (ceil_div(prob->d, c.lanes * v) > kMaxGridY) return CONV2D_ERR_UNSUPPORTED;
+    if (!conv_fits(c, prob->d, v)) return CONV2D_ERR_UNSUPPORTED;
     if (need && !workspace) return CONV2D_ERR_INVALID_ARGUMENT;
     if (workspace_bytes < need) return CONV2D_ERR_WORKSPACE_TOO_SMALL;
     ConvArgs a = {};
@@ -337,7 +352,7 @@ int causal_conv_step(const causal_conv_step_problem_t *prob, int dtype, const vo
     if (!x || !weight || !y || (prob->pool > 0 && !state)) return CONV2D_ERR_INVALID_ARGUMENT;
     if (!all_aligned(bytes_of(dtype), {x, state, weight, bias, y}) || !aligned(slots, 4)) return CONV2D_ERR_UNSUPPORTED;
     const int v = kConvChannels, lanes = lanes_for(prob->d, v);
-    if (ceil_div(prob->d, lanes * v) > kMaxGridY) return CONV2D_ERR_UNSUPPORTED;
+    if (ceil_div(prob->d, lanes * v) > kMaxGridY || !fits(ceil_div(prob->rows, 256 / lanes), 256)) return CONV2D_ERR_UNSUPPORTED;
     ConvStepArgs a = {prob->rows, prob->pool, prob->d, prob->silu, lanes, prob->x_row, x, weight, bias, slots, state, y};
     return status(launch_conv_step(dtype, prob->w, a,
                                    dim3((unsigned)ceil_div(prob->rows, 256 / lanes), (unsigned)ceil_div(prob->d, lanes * v)),
@@ -351,6 +366,7 @@ int selective_scan_workspace_size(const selective_scan_problem_t *prob, int dtyp
     if (!bytes) return CONV2D_ERR_INVALID_ARGUMENT;
     ScanPlan s;
     scan_plan(prob, false, &s);
+    if (!scan_fits(prob, s, false)) return CONV2D_ERR_UNSUPPORTED;
     *bytes = scan_bytes(s, false);
     return CONV2D_OK;
 }
@@ -369,6 +385,7 @@ int selective_scan(const selective_scan_problem_t *prob, int dtype, const void *
         return CONV2D_ERR_UNSUPPORTED;
     ScanPlan s;
     scan_plan(prob, false, &s);
+    if (!scan_fits(prob, s, false)) return CONV2D_ERR_UNSUPPORTED;
     const size_t need = scan_bytes(s, false);
     if (need && !workspace) return CONV2D_ERR_INVALID_ARGUMENT;
     if (workspace_bytes < need) return CONV2D_ERR_WORKSPACE_TOO_SMALL;
@@ -400,6 +417,7 @@ int selective_scan_grad_workspace_size(const selective_scan_problem_t *prob, int
     if (!bytes) return CONV2D_ERR_INVALID_ARGUMENT;
     ScanPlan s;
     scan_plan(prob, true, &s);
+    if (!scan_fits(prob, s, true)) return CONV2D_ERR_UNSUPPORTED;
     *bytes = scan_bytes(s, true);
     return CONV2D_OK;
 }
@@ -422,8 +440,8 @@ int selective_scan_grad(const selective_scan_problem_t *prob, int dtype, const v
         return CONV2D_ERR_UNSUPPORTED;
     ScanPlan s;
     scan_plan(prob, true, &s);
+    if (!scan_fits(prob, s, true)) return CONV2D_ERR_UNSUPPORTED;
     if (workspace_bytes < scan_bytes(s, true)) return CONV2D_ERR_WORKSPACE_TOO_SMALL;
-    if (prob->batch.tokens * prob->groups * prob->n > kMaxRows * 128) return CONV2D_ERR_UNSUPPORTED;
     ScanArgs a = scan_args(prob, s);
     a.x = x;
     a.dt = dt;
@@ -474,7 +492,7 @@ int selective_scan_step(const selective_scan_step_problem_t *p, int dtype, const
     if (!x || !dt || !A || !B || !C || !y || (p->pool > 0 && !state)) return CONV2D_ERR_INVALID_ARGUMENT;
     if (!all_aligned(bytes_of(dtype), {x, dt, B, C, z, y}) || !all_aligned(4, {A, D, dt_bias, state, slots}))
         return CONV2D_ERR_UNSUPPORTED;
-    if (ceil_div(p->d, 64) > kMaxGridY) return CONV2D_ERR_UNSUPPORTED;
+    if (ceil_div(p->d, 64) > kMaxGridY || !fits(ceil_div(p->rows, scan_step_rows(p->n)), 256)) return CONV2D_ERR_UNSUPPORTED;
     ScanStepArgs a = {p->rows, p->pool, p->d, p->n, p->groups, p->softplus, p->x_row, p->dt_row, p->b_row, p->c_row,
                       p->z_row, p->b_group, p->c_group, x, dt, B, C, z, A, D, dt_bias, slots, state, y};
     return status(launch_scan_step(dtype, a, (hipStream_t)stream));
@@ -491,9 +509,10 @@ int fp8_quantize(int form, int dtype, int m, int k, const void *x, long long x_r
     if (m == 0 || k == 0) return CONV2D_OK;
     if (!x || !q || !scale) return CONV2D_ERR_INVALID_ARGUMENT;
     if (!aligned(x, bytes_of(dtype)) || !aligned(q, 16) || !aligned(scale, 4)) return CONV2D_ERR_UNSUPPORTED;
-    if (form == FP8_TRANSPOSE && ceil_div(k, 64) > kMaxGridY) return CONV2D_ERR_UNSUPPORTED;
-    if (form == FP8_BLOCKS && ceil_div(m, kFp8Block) > kMaxGridY) return CONV2D_ERR_UNSUPPORTED;
-    if (ceil_div(k, kFp8Block) * m > kMaxRows * 16) return CONV2D_ERR_UNSUPPORTED;
+    const long long kb = ceil_div(k, kFp8Block), mb = ceil_div(m, kFp8Block);
+    if (form == FP8_ROWS && !fits(ceil_div(kb * m, 16), 256)) return CONV2D_ERR_UNSUPPORTED;
+    if (form == FP8_TRANSPOSE && (ceil_div(k, 64) > kMaxGridY || !fits(mb, 256))) return CONV2D_ERR_UNSUPPORTED;
+    if (form == FP8_BLOCKS && (mb > kMaxGridY || !fits(kb, 256))) return CONV2D_ERR_UNSUPPORTED;
     const Fp8QuantArgs a = {m, k, x_row, q_pitch, x, (uint8_t *)q, scale};
     return status(launch_fp8_quantize(form, dtype, a, (hipStream_t)stream));
 }
@@ -514,9 +533,13 @@ int fp8_matmul_workspace_size(const fp8_matmul_problem_t *prob, int dtype, size_
     const int r = check_matmul(prob, dtype);
     if (r != CONV2D_OK) return r;
     if (!bytes) return CONV2D_ERR_INVALID_ARGUMENT;
-    *bytes = 0;
-    if (prob->m > 0 && prob->n > 0)
-        *bytes = fp8_matmul_bytes(prob->m, prob->n, fp8_matmul_plan(prob->m, prob->n, prob->k, dtype));
+    size_t need = 0;
+    if (prob->m > 0 && prob->n > 0) {
+        const Fp8Plan plan = fp8_matmul_plan(prob->m, prob->n, prob->k, dtype);
+        if (!fp8_matmul_fits(prob->m, prob->n, prob->k, plan)) return CONV2D_ERR_UNSUPPORTED;
+        need = fp8_matmul_bytes(prob->m, prob->n, plan);
+    }
+    *bytes = need;
     return CONV2D_OK;
 }
 
@@ -532,6 +555,7 @@ int fp8_matmul(const fp8_matmul_problem_t *prob, int dtype, const void *a, const
         !aligned(workspace, 16))
         return CONV2D_ERR_UNSUPPORTED;
     const Fp8Plan plan = fp8_matmul_plan(prob->m, prob->n, prob->k, dtype);
+    if (!fp8_matmul_fits(prob->m, prob->n, prob->k, plan)) return CONV2D_ERR_UNSUPPORTED;
     const size_t need = fp8_matmul_bytes(prob->m, prob->n, plan);
     if (need && !workspace) return CONV2D_ERR_INVALID_ARGUMENT;
     if (workspace_bytes < need) return CONV2D_ERR_WORKSPACE_TOO_SMALL;

@@ -6,6 +6,10 @@
 
 namespace cnv {
 
+// A launch's threads along x: the device counts them in 32 bits.
+constexpr long long kMaxThreads = (1LL << 32) - 1;
+constexpr bool fits(long long workgroups, int threads) { return workgroups <= kMaxThreads / threads; }
+
 // ---- causal convolution (causal_conv.hip) -------------------------------------
 constexpr int kConvUnroll = 4;    // rows whose loads are issued together
 constexpr int kConvChannels = 4;  // channels per thread, where there are so many
@@ -87,6 +91,9 @@ constexpr int scan_step_tokens(int n) { return n <= 16 ? 16 : n <= 32 ? 8 : 4; }
 // four sequences of 2048 with 2048 channels).
 constexpr int scan_grad_step_tokens(int n) { return n <= 8 ? 16 : n <= 16 ? 8 : 4; }
 
+// Rows a thread of the single-token kernel takes where there are many.
+constexpr int scan_step_rows(int n) { return n > 16 ? 2 : 4; }
+
 hipError_t launch_scan(int dtype, const ScanArgs &a, int waves, hipStream_t st);
 hipError_t launch_scan_grad(int dtype, const ScanArgs &a, hipStream_t st);
 hipError_t launch_scan_step(int dtype, const ScanStepArgs &a, hipStream_t st);
@@ -122,6 +129,7 @@ struct Fp8Plan {
 
 hipError_t launch_fp8_quantize(int form, int dtype, const Fp8QuantArgs &a, hipStream_t st);
 Fp8Plan fp8_matmul_plan(int m, int n, int k, int dtype);
+bool fp8_matmul_fits(int m, int n, int k, const Fp8Plan &p);  // whether its launches fit
 size_t fp8_matmul_bytes(int m, int n, const Fp8Plan &p);
 hipError_t launch_fp8_matmul(int dtype, const Fp8MatmulArgs &a, const Fp8Plan &p, void *workspace, hipStream_t st);
 

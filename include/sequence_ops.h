@@ -8,6 +8,9 @@
  *     enqueued on `stream` (a hipStream_t, NULL = the null stream).
  *   - Status codes are those of conv2d_nhwc.h; every check runs before anything
  *     is enqueued, and on error no output byte is written.
+ *     Sizes whose launches the device cannot take (2^32 threads along an axis:
+ *     2^26 chunks of 16 channels of a scan, 2^32 values of dB, 2^28 blocks of
+ *     an fp8 operand) are CONV2D_ERR_UNSUPPORTED among those checks.
  *   - Results are the same bits on every run: no atomics on values, every
  *     reduction in a fixed order.  Sums, states and gradients' partial sums
  *     are fp32; each output is rounded once, to nearest even.
