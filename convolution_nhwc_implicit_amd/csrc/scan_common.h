@@ -88,6 +88,11 @@ __device__ inline float softplus_f32(float raw)
     return raw != raw ? raw : r;  // the maximum above drops a NaN
 }
 
+// A rate as it is used: at most 2e38 in size, so that the decay exp(delta A) of
+// an infinite one is still 0 (or infinite), but 1 for tokens that are not there
+// (delta = 0), where 0 times infinity would spoil the state behind them.
+__device__ inline float finite_rate(float A) { return A < -2e38f ? -2e38f : A > 2e38f ? 2e38f : A; }
+
 // The chunk that a workgroup walks.
 struct Chunk {
     int s;            // sequence

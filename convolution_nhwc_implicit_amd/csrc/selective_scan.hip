@@ -87,7 +87,7 @@ __global__ __launch_bounds__(waves * 64, 2) void scan_kernel(ScanArgs a)
     at.load(a.A, 0, A2);
 #pragma unroll
     for (int j = 0; j < NL; ++j) {
-        A2[j] *= kLog2e;
+        A2[j] = finite_rate(A2[j]) * kLog2e;
         first[j] = 0.0f;
     }
     if (!LOCAL) {
@@ -272,7 +272,7 @@ __global__ __launch_bounds__(256) void scan_join_kernel(ScanArgs a)
     const long long i = (long long)blockIdx.y * 256 + threadIdx.x, per = (long long)a.d * a.n;
     if (i >= per) return;
     const long long ch = i / a.n;
-    const float A2 = a.A[i] * kLog2e;
+    const float A2 = finite_rate(a.A[i]) * kLog2e;
     // Eight chunks' values are loaded together: one after the other, each would
     // wait for memory.
     constexpr int AHEAD = 8;
@@ -341,7 +341,7 @@ __global__ __launch_bounds__(256) void scan_step_kernel(ScanStepArgs a)
     read_nl<NL>(a.A + (long long)ch * a.n, a.n, part, A2);
     const float bias = a.dt_bias ? a.dt_bias[ch] : 0.0f, D = a.D ? a.D[ch] : 0.0f;
 #pragma unroll
-    for (int j = 0; j < NL; ++j) A2[j] *= kLog2e;
+    for (int j = 0; j < NL; ++j) A2[j] = finite_rate(A2[j]) * kLog2e;
 #pragma unroll
     for (int u = 0; u < R; ++u) {
         if (r0 + u >= a.rows) break;

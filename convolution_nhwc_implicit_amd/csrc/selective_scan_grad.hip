@@ -80,7 +80,7 @@ __global__ __launch_bounds__(256) void scan_keep_kernel(ScanArgs a)
     at.load(a.A, 0, A2);
 #pragma unroll
     for (int j = 0; j < NL; ++j) {
-        A2[j] *= kLog2e;
+        A2[j] = finite_rate(A2[j]) * kLog2e;
         h[j] = back[j] = 0.0f;
         P[j] = 1.0f;
     }
@@ -180,7 +180,10 @@ __global__ __launch_bounds__(256, NL > 8 ? 1 : 2) void scan_back_kernel(ScanArgs
     float A[NL], carry[NL], H0[NL], dA[NL], sum_D = 0.0f, sum_bias = 0.0f;
     at.load(a.A, 0, A);
 #pragma unroll
-    for (int j = 0; j < NL; ++j) dA[j] = carry[j] = H0[j] = 0.0f;
+    for (int j = 0; j < NL; ++j) {
+        A[j] = finite_rate(A[j]);
+        dA[j] = carry[j] = H0[j] = 0.0f;
+    }
     const bool joined = a.chunk_state != nullptr;
     if (k.valid) {
         if (joined) {

@@ -121,6 +121,10 @@ int causal_conv_step(const causal_conv_step_problem_t *prob, int dtype, const vo
  *   initial_state and final_state [seqs][d][n] (may be NULL): fp32, dense.  The
  *             states must not overlap.
  *   y [tokens][d] dense, dtype; must not overlap the inputs.
+ * Rates of A past 2e38 in size, infinite ones among them, count as 2e38: their
+ * decays are 0 where delta > 0 and 1 where delta = 0.  Decays are also multiplied
+ * over runs of tokens before they meet a state: for growing states (delta * A > 0)
+ * results are NaN where such a product is infinite and the state is 0.
  * 1 <= n <= 64; groups divides d.  Row strides and d are below 2^24.
  * Long sequences are cut into chunks that run side by side, joined through the
  * workspace (selective_scan_workspace_size; 16-byte aligned; the size may be 0).

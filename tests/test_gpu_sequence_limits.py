@@ -70,3 +70,40 @@ def test_scan_grad_past_31_bits():
     for k in ("dB", "dC"):
         a, b = whole[k][4].float(), last[k][0].float()
         assert ((a - b).abs() <= 2.0 ** -7 * b.abs() + 2.0 ** -6 * d ** 0.5).all(), k
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_infinite_rates(packed):
+    """A of minus infinity forgets the state at every token, also where a chunk ends inside a step: h = delta x B."""
+    L, d, n = 300, 20, 16
+    g = torch.Generator(device=DEV).manual_seed(6)
+    lead = (2 * L + 3,) if packed else (2, L)
+    start = torch.tensor([0, L, 2 * L + 3], dtype=torch.int32, device=DEV) if packed else None
+    x, dt, dy = (torch.randn(*lead, d, generator=g, device=DEV) for _ in range(3))
+    B, C = (torch.randn(*lead, 1, n, generator=g, device=DEV) for _ in range(2))
+    A = -torch.rand(d, n, generator=g, device=DEV)
+    A[:, 3] = -float("inf")
+    A[5] = -float("inf")
+    dfinal = torch.randn(2, d, n, generator=g, device=DEV)
+    kw = dict(softplus=True, seq_start=start)
+    y, final = nn.selective_scan(x, dt, A, B, C, return_state=True, **kw)
+    got = nn.selective_scan_grad(dy, x, dt, A, B, C, dfinal_state=dfinal, **kw)
+    assert y.isfinite().all() and all(v.isfinite().all() for v in got.values() if v is not None)
+    ends = [L - 1, 2 * L + 2] if packed else None
+    xe, de, Be = ((t[ends] if packed else t[:, -1]) for t in (x, torch.nn.functional.softplus(dt.double()), B))
+    want = (de * xe).unsqueeze(-1) * Be.double()
+    bound = 16 * R.U * want.abs() + 1e-30  # the step size's roundings and two products
+    for c, k in ((slice(None), 3), (5, slice(None))):
+        assert ((final.double() - want).abs() <= bound)[:, c, k].all()
+    # no such rate takes part in what lies beside it
+    A2 = A.clone()
+    A2[:, 3] = -2e38
+    A2[5] = -2e38
+    y2, final2 = nn.selective_scan(x, dt, A2, B, C, return_state=True, **kw)
+    assert torch.equal(y, y2) and torch.equal(final, final2)
+    state, pool = torch.randn(4, d, n, generator=g, device=DEV), (x[:4] if packed else x[0, :4])
+    t = [v[:4] if packed else v[0, :4] for v in (dt, B, C)]
+    other = state.clone()
+    assert torch.equal(nn.selective_scan_step(pool, t[0], A, t[1], t[2], state, softplus=True),
+                       nn.selective_scan_step(pool, t[0], A2, t[1], t[2], other, softplus=True))
+    assert torch.equal(state, other)
