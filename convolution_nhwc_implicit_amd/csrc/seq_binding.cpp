@@ -9,6 +9,7 @@
 // Types, shapes and strides are checked before the devices, so that a wrong call
 // says what is wrong with it on any machine.
 #include <ATen/ATen.h>
+#include <ATen/core/grad_mode.h>
 #include <ATen/hip/impl/HIPStreamMasqueradingAsCUDA.h>
 #include <c10/core/DeviceGuard.h>
 #include <torch/csrc/Dtype.h>
@@ -105,6 +106,17 @@ struct Checks {
             if (seen[i]->device() != first.device())
                 value_error(string(names[i]) + " must be on " + first.device().str() + ", got " + seen[i]->device().str());
         }
+    }
+    // Results carry no gradient history: a warning where a caller may expect one.
+    void detached(const char *where, const char *instead) const
+    {
+        if (!at::GradMode::is_enabled()) return;
+        for (int i = 0; i < count; ++i)
+            if (seen[i]->requires_grad()) {
+                const string m = string(where) + ": " + names[i] + " requires a gradient, but the result carries no gradient history; " + instead;
+                if (PyErr_WarnEx(PyExc_UserWarning, m.c_str(), 2) < 0) throw python_error();
+                return;
+            }
     }
 };
 
@@ -265,6 +277,7 @@ PyObject *py_causal_conv(PyObject *, PyObject *const *a, Py_ssize_t n)
     Conv v(a);
     const bool state = truth(a[6]);
     v.c.device(*v.x);
+    v.c.detached("causal_conv", "causal_conv_grad computes the gradients");
     const c10::DeviceGuard guard(v.x->device());
     const Tensor y = new_tensor(*v.x, v.x->sizes(), v.x->scalar_type());
     const Tensor f = state ? new_tensor(*v.x, {v.seqs, v.w - 1, v.d}, v.x->scalar_type()) : Tensor();
@@ -329,6 +342,7 @@ PyObject *py_causal_conv_step(PyObject *, PyObject *const *a, Py_ssize_t n)
     const causal_conv_step_problem_t p = {int_size(rows, "rows"), int_size(pool, "pool"), int_size(d, "d"),
                                           int_size(w, "w"), silu, row_stride(*x)};
     c.device(*x);
+    c.detached("causal_conv_step", "causal_conv and causal_conv_grad compute prompts and their gradients");
     const c10::DeviceGuard guard(x->device());
     const Tensor y = new_tensor(*x, {rows, d}, type);
     raise(causal_conv_step(&p, code, ptr(x), state->data_ptr(), ptr(weight), ptr(bias), sp, out_ptr(y), stream_of(*x)),
@@ -404,6 +418,7 @@ PyObject *py_selective_scan(PyObject *, PyObject *const *a, Py_ssize_t n)
     ScanTokens v(a);
     const bool state = truth(a[11]);
     v.c.device(*v.x);
+    v.c.detached("selective_scan", "selective_scan_grad computes the gradients");
     const c10::DeviceGuard guard(v.x->device());
     size_t need = 0;
     raise(selective_scan_workspace_size(&v.p, v.code, &need), "selective_scan_workspace_size");
@@ -473,6 +488,7 @@ PyObject *py_selective_scan_step(PyObject *, PyObject *const *a, Py_ssize_t n)
         soft, row_stride(*v.x), row_stride(*v.dt), row_stride(*v.B), row_stride(*v.C), v.z ? row_stride(*v.z) : 0,
         v.group_stride(*v.B), v.group_stride(*v.C)};
     v.c.device(*v.x);
+    v.c.detached("selective_scan_step", "selective_scan and selective_scan_grad compute prompts and their gradients");
     const c10::DeviceGuard guard(v.x->device());
     const Tensor y = new_tensor(*v.x, {rows, v.d}, v.x->scalar_type());
     raise(selective_scan_step(&p, v.code, ptr(v.x), ptr(v.dt), (const float *)ptr(v.A), ptr(v.B), ptr(v.C),
@@ -497,6 +513,7 @@ PyObject *py_fp8_quantize(PyObject *, PyObject *const *a, Py_ssize_t n)
     Checks c;
     c.strided(*x, "x", x->scalar_type(), x->sizes());
     c.device(*x);
+    c.detached("fp8_quantize", "rounding to 8 bits has none");
     const int64_t m = x->size(0), k = x->size(1), rows = transpose ? k : m, cols = transpose ? m : k;
     const int64_t pitch = (cols + 127) / 128 * 128;  // whole lines: rows that straddle them cost the products' loads
     const c10::DeviceGuard guard(x->device());
@@ -539,6 +556,7 @@ PyObject *py_fp8_matmul(PyObject *, PyObject *const *a, Py_ssize_t n)
     if (w->size(1) != x->size(1))
         value_error("b must be [n][" + std::to_string(x->size(1)) + "], got " + shape_text(w->sizes()));
     c.device(*x);
+    c.detached("fp8_matmul", "the gradients are products of the same kind");
     const fp8_matmul_problem_t p = {int_size(x->size(0), "m"), int_size(w->size(0), "n"), int_size(x->size(1), "k"), blocks, xp, wp};
     const int code = type == at::kHalf ? CONV2D_DTYPE_F16 : type == at::kBFloat16 ? CONV2D_DTYPE_BF16 : CONV2D_DTYPE_F32;
     const c10::DeviceGuard guard(x->device());

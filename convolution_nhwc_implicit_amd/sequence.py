@@ -15,6 +15,9 @@ axis and may be slices of a wider projection's output.  ``seq_start`` is not
 read on the host: it must rise from 0 to T; rows outside every sequence stay
 unspecified.
 
+Gradients are calls of their own: results carry no autograd history.  With
+gradients enabled, an input that requires one draws a UserWarning.
+
 Wrong types raise TypeError, wrong shapes, strides and devices ValueError, and
 what the kernels do not support Conv2dError, before anything is enqueued.
 """
