@@ -129,6 +129,12 @@ void *stream_of(const Tensor &t)
     return (void *)c10::hip::getCurrentHIPStreamMasqueradingAsCUDA(t.device().index()).stream();
 }
 
+// A step has written to it: what autograd saved of it before is not its value any more.
+void written(const Tensor &t)
+{
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 Tensor new_tensor(const Tensor &like, at::IntArrayRef shape, at::ScalarType type)
 {
     return at::empty(shape, like.options().dtype(type).requires_grad(false));
@@ -347,6 +353,7 @@ PyObject *py_causal_conv_step(PyObject *, PyObject *const *a, Py_ssize_t n)
     const Tensor y = new_tensor(*x, {rows, d}, type);
     raise(causal_conv_step(&p, code, ptr(x), state->data_ptr(), ptr(weight), ptr(bias), sp, out_ptr(y), stream_of(*x)),
           "causal_conv_step");
+    written(*state);
     return wrap(y);
     END_HANDLE_TH_ERRORS
 }
@@ -494,6 +501,7 @@ PyObject *py_selective_scan_step(PyObject *, PyObject *const *a, Py_ssize_t n)
     raise(selective_scan_step(&p, v.code, ptr(v.x), ptr(v.dt), (const float *)ptr(v.A), ptr(v.B), ptr(v.C),
                               (const float *)ptr(v.D), ptr(v.z), (const float *)ptr(v.bias), (float *)state->data_ptr(), sp,
                               out_ptr(y), stream_of(*v.x)), "selective_scan_step");
+    written(*state);
     return wrap(y);
     END_HANDLE_TH_ERRORS
 }

@@ -1,4 +1,5 @@
-"""The sequence operators beside autograd: inputs that require a gradient are not dropped without a word."""
+"""The sequence operators beside autograd: inputs that require a gradient are not dropped without a word, and states
+that a step writes in place count as written."""
 import warnings
 
 import pytest
@@ -61,3 +62,23 @@ def test_gradient_calls_take_parameters():
         assert not any(v is not None and v.requires_grad for v in got.values())
         conv = {k: v.clone().requires_grad_() for k, v in CALLS["causal_conv"][0].items()}
         assert not nn.causal_conv_grad(t(5, 8), **conv)["dw"].requires_grad
+
+
+@pytest.mark.parametrize("name", ["causal_conv_step", "selective_scan_step"])
+def test_steps_count_as_writes(name):
+    args, _ = CALLS[name]
+    state = args["state"].clone()
+    before = state._version
+    view = state[:]
+    getattr(nn, name)(**{**args, "state": state})
+    assert state._version > before and view._version == state._version
+    # what autograd saved of a state before a step is not used after it
+    w = torch.ones_like(state, requires_grad=True)
+    out = (w * state).sum()
+    getattr(nn, name)(**{**args, "state": state})
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        out.backward()
+    with torch.inference_mode():
+        inner = state.clone()
+        getattr(nn, name)(**{**args, "state": inner})
+    getattr(nn, name)(**{**args, "state": inner})  # an inference tensor has no version
