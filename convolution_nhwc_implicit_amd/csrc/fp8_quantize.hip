@@ -2,7 +2,8 @@
 //
 // One read of x and one write of q: bound by memory.  A block's scale needs its
 // largest value first, so the block waits in registers (or, transposed, in LDS)
-// between the two.  4057 x 4104 bf16 by rows: 11 us (4.6 TB/s).
+// between the two.  4057 x 4104 bf16 by rows: 11 us (4.6 TB/s); 8200 x 4104 by
+// blocks of 128 x 128: 25 us (4.1 TB/s).
 #include "seq_common.h"
 #include "seq_internal.h"
 

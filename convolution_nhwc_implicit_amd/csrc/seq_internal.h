@@ -84,7 +84,10 @@ struct ScanStepArgs {
 };
 
 // Tokens a wave takes at once: as many as keep the loads of the next ones under
-// way without filling the registers.
+// way.  A run's decays and inputs take 128 registers for any n above 8; what is
+// read ahead of B and C grows with n and spills past 16 states (3 to 19 registers
+// up to 32, 55 to 88 up to 64): 4096 tokens of 2048 channels take 102 us with 16
+// states, 265 with 32, 1270 with 64.
 constexpr int scan_step_tokens(int n) { return n <= 16 ? 16 : n <= 32 ? 8 : 4; }
 // The gradient keeps a step's decays and states in registers, TS * n/4 values of
 // each: 64 registers of each would spill (16 tokens of 16 states: 1115 us for

@@ -81,8 +81,9 @@ def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, softplus=False,
     delta = softplus(dt + dt_bias) (or the sum itself).
 
     x, dt, z [..][d] and B, C [..][groups][n] in one type, A [d][n], D [d], dt_bias [d] and the states
-    [seqs][d][n] in float32; channel c belongs to group c // (d / groups); n <= 64.  With return_state
-    the result is (y, final_state)."""
+    [seqs][d][n] in float32; channel c belongs to group c // (d / groups); n <= 64, fastest up to 16.
+    Rates of A past 2e38 in size (infinite ones) count as 2e38.  With return_state the result is
+    (y, final_state)."""
     return load().selective_scan(x, dt, A, B, C, D, z, dt_bias, softplus, initial_state, seq_start, return_state)
 
 
@@ -108,8 +109,9 @@ def fp8_quantize(x, transpose=False, blocks=False):
 
     transpose: of x's transpose, q [k][m] and scale [k][ceil(m/128)].  blocks: a scale for every 128 x 128
     values (weights), scale [ceil(m/128)][ceil(k/128)].  Scales are the least powers of two (at least 2^-126)
-    that bring a block's finite values into e4m3's range; infinities and NaN become NaN.  q's rows are padded
-    with zeros to a multiple of 128 bytes; q is a view of them."""
+    that bring a block's finite values into e4m3's range (2^-126 for a block of zeros, which costs fp8_matmul
+    time); infinities and NaN become NaN.  q's rows are padded with zeros to a multiple of 128 bytes; q is a
+    view of them."""
     return load().fp8_quantize(x, transpose, blocks)
 
 
@@ -117,6 +119,7 @@ def fp8_matmul(a, a_scale, b, b_scale, out_dtype=torch.bfloat16):
     """a times b's transpose: out [m][n] in out_dtype (float16, bfloat16 or float32) of e4m3 operands a [m][k]
     and b [n][k] with float32 scales of 128 values along k: a_scale [m][ceil(k/128)], and b_scale
     [n][ceil(k/128)] or [ceil(n/128)][ceil(k/128)].  Scales may be any values; powers of two from 2^-62 to 2^62
-    cost no time.  Sums are float32, rounded once; for a 16-bit result the fp8 matrix unit cuts each group of 8
-    neighbouring products at 2^-13 of its largest, well below the result's own rounding."""
+    cost no time, others more than double it.  Sums are float32, rounded once; for a 16-bit result the fp8 matrix unit
+    cuts each group of 8 neighbouring products at 2^-13 of its largest, below the result's own rounding (a float32
+    result has no such cut, and may be rounded afterwards)."""
     return load().fp8_matmul(a, a_scale, b, b_scale, out_dtype)

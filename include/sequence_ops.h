@@ -13,7 +13,8 @@
  *     an fp8 operand) are CONV2D_ERR_UNSUPPORTED among those checks.
  *   - Results are the same bits on every run: no atomics on values, every
  *     reduction in a fixed order.  Sums, states and gradients' partial sums
- *     are fp32; each output is rounded once, to nearest even.
+ *     are fp32 (of fp8 products see there); each output is rounded once, to
+ *     nearest even.
  *   - Buffers need the alignment of their elements only, unless stated.
  *   - "rows" are tokens.  A tensor of rows has unit stride over its last
  *     axis; its strides between rows and between sequences are in elements.
@@ -38,8 +39,8 @@ extern "C" {
  * [seqs][len]; otherwise they lie packed, sequence s in rows
  * seq_start[s] .. seq_start[s+1]-1 of `tokens` rows (0 = first, tokens = last
  * value, not descending; empty sequences allowed).  seq_start is read on the
- * device: values outside 0..tokens are clamped, never followed, and rows that
- * no sequence covers are left unwritten.
+ * device: values outside 0..tokens are clamped, never followed.  Results of rows
+ * that no sequence covers are unspecified, and all of them where starts descend.
  */
 typedef struct seq_batch {
     const int *seq_start; /* device, [seqs + 1], or NULL */
@@ -208,10 +209,20 @@ int fp8_quantize(int form, int dtype, int m, int k, const void *x, long long x_r
 
 /*
  * out[i][j] = sum_k a[i][k] a_scale[i][k/128] * b[j][k] b_scale[j or j/128][k/128],
- * summed in fp32, rounded once to dtype (CONV2D_DTYPE_F16, _BF16 or _F32).
+ * rounded once to dtype (CONV2D_DTYPE_F16, _BF16 or _F32).
+ * dtype _F32: products are exact and summed in fp32.  16-bit dtypes use the fp8
+ * matrix unit at twice the rate, which cuts each of 8 neighbouring products of a
+ * block at 2^-13 of the largest's power of two before it adds them; sums of such
+ * groups, of blocks and of parts of k are fp32.  In norm the cut is 1.5e-5 of a
+ * block's sum, below the result's own rounding (1.7e-3 bf16, 2e-4 fp16): on
+ * normal data 1.5 of a hundred bf16 results, and 8 of fp16, round to a neighbour
+ * of what fp32 sums give.  A 16-bit result of exact products is the _F32 one,
+ * rounded.
  *   a [m][k] with pitch a_pitch, a_scale [m][ceil(k/128)]
  *   b [n][k] with pitch b_pitch, b_scale [n][ceil(k/128)], or with b_blocks = 1
- *     [ceil(n/128)][ceil(k/128)]; scales are any fp32 values
+ *     [ceil(n/128)][ceil(k/128)].  Scales are any fp32 values; a block's sum
+ *     times a's scale has to stay in fp32's range.  Tiles all of whose scales are
+ *     powers of two from 2^-62 to 2^62 take one walk along k, others three.
  *   out [m][n] dense; must not overlap the operands
  * a and b are 16-byte aligned, their pitches multiples of 16; bytes past a row's
  * end are read but have no influence.  The workspace (fp8_matmul_workspace_size;
