@@ -221,7 +221,7 @@ int fp8_quantize(int form, int dtype, int m, int k, const void *x, long long x_r
  *   a [m][k] with pitch a_pitch, a_scale [m][ceil(k/128)]
  *   b [n][k] with pitch b_pitch, b_scale [n][ceil(k/128)], or with b_blocks = 1
  *     [ceil(n/128)][ceil(k/128)].  Scales are any fp32 values; a block's sum
- *     times a's scale has to stay in fp32's range.  Tiles all of whose scales are
+ *     times either operand's has to stay in fp32's range.  Tiles all of whose scales are
  *     powers of two from 2^-62 to 2^62 take one walk along k, others three.
  *   out [m][n] dense; must not overlap the operands
  * a and b are 16-byte aligned, their pitches multiples of 16; bytes past a row's
