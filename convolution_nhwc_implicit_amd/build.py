@@ -26,7 +26,8 @@ ARCH = "gfx950"
 
 SOURCES = ["api.cpp", "igemm.hip", "band.hip", "wino.hip", "wgrad.hip", "wgrad_band.hip", "direct.hip", "repack.hip", "fewchan.hip", "fewchan_wgrad.hip", "fewchan_dgrad.hip", "pointwise.hip", "pointwise_wgrad.hip", "patch.hip",
            "seq_api.cpp", "causal_conv.hip", "selective_scan.hip", "selective_scan_grad.hip",
-           "fp8_quantize.hip", "fp8_matmul.hip"]
+           "fp8_quantize.hip", "fp8_matmul.hip", "block_api.cpp", "column_sums.hip", "layer_norm.hip", "layer_norm_grad.hip",
+           "gated_recurrence.hip", "gated_recurrence_grad.hip", "fp4.hip"]
 
 COMMON_FLAGS = [
     "-x", "hip", f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",

@@ -1,0 +1,357 @@
+// block_api.cpp -- the C ABI of a recurrent block's operators (gated recurrence, layer
+// norm, 4-bit products): argument checks, workspace layout, launch shapes.
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+
+#include "block_internal.h"
+#include "seq_checks.h"
+
+using namespace cnv;
+
+namespace {
+
+// ---- gated recurrence --------------------------------------------------------------
+int check_recurrence(const gated_recurrence_problem_t *p, int dtype, bool grad)
+{
+    if (!p) return CONV2D_ERR_INVALID_ARGUMENT;
+    int r = check_batch(p->batch);
+    if (r != CONV2D_OK) return r;
+    if (p->d < 1) return CONV2D_ERR_INVALID_ARGUMENT;
+    for (const seq_stride_t *s : {&p->x, &p->r, &p->i, &p->z})
+        if (r == CONV2D_OK) r = check_stride(*s);
+    if (r == CONV2D_OK && grad) r = check_stride(p->dy);
+    if (r != CONV2D_OK) return r;
+    if (!float_type(dtype) || p->d > kMaxStride || ceil_div(p->d, kRecurChannels) > kMaxGridY) return CONV2D_ERR_UNSUPPORTED;
+    return CONV2D_OK;
+}
+
+struct RecurPlan {
+    int chunk, chunks, joined;
+    size_t per_chunk, per_segment;  // bytes of a value for each of them and channel
+};
+
+// Tokens of a chunk: sequences stay whole where that alone fills the chip (a workgroup
+// to a compute unit), since cut ones are read twice; else about two workgroups to each.
+RecurPlan recur_plan(const gated_recurrence_problem_t *p, int segment)
+{
+    const seq_batch_t &b = p->batch;
+    const long long across = ceil_div(p->d, kRecurChannels);
+    long long chunk;
+    if (!b.seq_start && b.len > 0 && b.len % segment == 0 && b.len <= kRecurChunkMost && across * b.seqs >= kCUs)
+        chunk = b.len;
+    else
+        chunk = ceil_div(ceil_div(b.tokens, ceil_div(2 * kCUs, across)), segment) * segment;
+    chunk = std::min<long long>(std::max<long long>(chunk, segment), kRecurChunkMost);
+    RecurPlan r;
+    r.chunk = (int)chunk;
+    r.chunks = (int)ceil_div(b.tokens, chunk);
+    r.joined = r.chunks > 1 && (b.seq_start || chunk % b.len != 0);
+    r.per_chunk = up((size_t)r.chunks * p->d * 4);
+    r.per_segment = up((size_t)r.chunks * (chunk / segment) * p->d * 4);
+    return r;
+}
+size_t recur_bytes(const RecurPlan &r) { return r.joined ? 2 * r.per_chunk : 0; }
+size_t recur_grad_bytes(const gated_recurrence_problem_t *p, const RecurPlan &r)
+{
+    return up((size_t)r.chunks * 3 * p->d * 4) + 2 * r.per_segment + (r.joined ? 4 * r.per_chunk : 0);
+}
+// launches: 512 threads a chunk, and for 256 sequences
+bool recur_fits(const gated_recurrence_problem_t *p, const RecurPlan &r)
+{
+    return fits((long long)r.chunks + ceil_div(p->batch.seqs, kRecurStateSeqs), 64 * 16);
+}
+
+RecurArgs recur_args(const gated_recurrence_problem_t *p, const RecurPlan &r)
+{
+    RecurArgs a = {};
+    a.q = seqs_of(p->batch);
+    a.d = p->d;
+    a.chunk = r.chunk;
+    a.chunks = r.chunks;
+    a.joined = r.joined;
+    a.xs = stride_of(p->x);
+    a.rs = stride_of(p->r);
+    a.is = stride_of(p->i);
+    a.zs = stride_of(p->z);
+    a.dys = stride_of(p->dy);
+    return a;
+}
+
+// ---- layer norm --------------------------------------------------------------------
+int check_norm(const layer_norm_problem_t *p, int dtype, int param_dtype)
+{
+    if (!p || p->seqs < 0 || p->len < 0 || p->d < 1 || !(p->eps >= 0.0f)) return CONV2D_ERR_INVALID_ARGUMENT;
+    for (const seq_stride_t *s : {&p->x, &p->residual, &p->dy, &p->dtotal})
+        if (s->row < 0 || s->seq < 0) return CONV2D_ERR_INVALID_ARGUMENT;
+    if (!std::isfinite(p->eps)) return CONV2D_ERR_INVALID_ARGUMENT;
+    if (!float_type(dtype) || (param_dtype != dtype && param_dtype != CONV2D_DTYPE_F32)) return CONV2D_ERR_UNSUPPORTED;
+    return p->d > kMaxStride || (long long)p->seqs * p->len > kMaxRows ? CONV2D_ERR_UNSUPPORTED : CONV2D_OK;
+}
+
+// Whether a launch with each row in a shape's lanes fits.
+bool norm_fits(const NormShape &s, long long rows) { return fits(ceil_div(rows * s.lanes, 256), 256); }
+
+NormArgs norm_args(const layer_norm_problem_t *p, int param_dtype)
+{
+    NormArgs a = {};
+    a.rows = p->seqs * p->len;
+    a.len = p->len;
+    a.d = p->d;
+    a.eps = p->eps;
+    a.count = (float)p->d;
+    a.param_f32 = param_dtype == CONV2D_DTYPE_F32;
+    a.xs = stride_of(p->x);
+    a.rs = stride_of(p->residual);
+    a.dys = stride_of(p->dy);
+    a.dts = stride_of(p->dtotal);
+    return a;
+}
+
+struct NormGradPlan {
+    NormShape shape;
+    int per, parts;
+    size_t partial, stats;
+};
+// Parts of rows, each with a partial sum of both parameters' gradients: as many as
+// give every compute unit a few workgroups, and no more, for they are written and read.
+NormGradPlan norm_grad_plan(const layer_norm_problem_t *p, int dtype)
+{
+    NormGradPlan r;
+    r.shape = layer_norm_grad_shape(dtype, p->d);
+    const long long rows = (long long)p->seqs * p->len;
+    const int groups = r.shape.held ? std::max(1, 256 / r.shape.lanes) : 1;
+    r.per = (int)(ceil_div(ceil_div(std::max(rows, 1LL), 2 * kCUs), groups) * groups);
+    r.parts = (int)ceil_div(rows, r.per);
+    r.partial = up((size_t)r.parts * 2 * p->d * 4);
+    r.stats = r.shape.held ? 0 : up((size_t)rows * 16);
+    return r;
+}
+
+}  // namespace
+
+extern "C" {
+
+int gated_recurrence_workspace_size(const gated_recurrence_problem_t *prob, int dtype, size_t *bytes)
+{
+    const int r = check_recurrence(prob, dtype, false);
+    if (r != CONV2D_OK) return r;
+    if (!bytes) return CONV2D_ERR_INVALID_ARGUMENT;
+    const RecurPlan plan = recur_plan(prob, kRecurSegment);
+    if (!recur_fits(prob, plan)) return CONV2D_ERR_UNSUPPORTED;
+    *bytes = recur_bytes(plan);
+    return CONV2D_OK;
+}
+
+int gated_recurrence(const gated_recurrence_problem_t *prob, int dtype, const void *x, const void *r, const void *i,
+                     const float *A, const void *z, const float *r_bias, const float *i_bias, const float *initial_state,
+                     void *y, float *final_state, void *workspace, size_t workspace_bytes, void *stream)
+{
+    const int e = check_recurrence(prob, dtype, false);
+    if (e != CONV2D_OK) return e;
+    const bool rows = prob->batch.tokens > 0;
+    if (!A || (rows && (!x || !r || !i || !y))) return CONV2D_ERR_INVALID_ARGUMENT;
+    if (!all_aligned(bytes_of(dtype), {x, r, i, z, y}) || !all_aligned(4, {A, r_bias, i_bias, initial_state, final_state}) ||
+        !aligned(workspace, 16))
+        return CONV2D_ERR_UNSUPPORTED;
+    const RecurPlan plan = recur_plan(prob, kRecurSegment);
+    if (!recur_fits(prob, plan)) return CONV2D_ERR_UNSUPPORTED;
+    const size_t need = recur_bytes(plan);
+    if (need && !workspace) return CONV2D_ERR_INVALID_ARGUMENT;
+    if (workspace_bytes < need) return CONV2D_ERR_WORKSPACE_TOO_SMALL;
+    if (!rows && !final_state) return CONV2D_OK;
+    RecurArgs a = recur_args(prob, plan);
+    a.x = x;
+    a.r = r;
+    a.i = i;
+    a.z = z;
+    a.A = A;
+    a.r_bias = r_bias;
+    a.i_bias = i_bias;
+    a.initial = initial_state;
+    a.y = y;
+    a.final_state = final_state;
+    if (plan.joined) {
+        Carver w{(char *)workspace};
+        a.chunk_decay = w.take(plan.per_chunk);
+        a.chunk_state = w.take(plan.per_chunk);
+    }
+    return status(launch_recurrence(dtype, a, (hipStream_t)stream));
+}
+
+int gated_recurrence_grad_workspace_size(const gated_recurrence_problem_t *prob, int dtype, size_t *bytes)
+{
+    const int r = check_recurrence(prob, dtype, true);
+    if (r != CONV2D_OK) return r;
+    if (!bytes) return CONV2D_ERR_INVALID_ARGUMENT;
+    const RecurPlan plan = recur_plan(prob, kRecurGradSegment);
+    if (!recur_fits(prob, plan)) return CONV2D_ERR_UNSUPPORTED;
+    *bytes = recur_grad_bytes(prob, plan);
+    return CONV2D_OK;
+}
+
+int gated_recurrence_grad(const gated_recurrence_problem_t *prob, int dtype, const void *dy, const void *x, const void *r,
+                          const void *i, const float *A, const void *z, const float *r_bias, const float *i_bias,
+                          const float *initial_state, const float *dfinal, const gated_recurrence_grads_t *g,
+                          void *workspace, size_t workspace_bytes, void *stream)
+{
+    const int e = check_recurrence(prob, dtype, true);
+    if (e != CONV2D_OK) return e;
+    const bool rows = prob->batch.tokens > 0;
+    if (!A || !g || !g->dA) return CONV2D_ERR_INVALID_ARGUMENT;
+    if (rows && (!dy || !x || !r || !i || !g->dx || !g->dr || !g->di || (z && !g->dz))) return CONV2D_ERR_INVALID_ARGUMENT;
+    if (!all_aligned(bytes_of(dtype), {dy, x, r, i, z, g->dx, g->dr, g->di, g->dz}) ||
+        !all_aligned(4, {A, r_bias, i_bias, initial_state, dfinal, g->dA, g->dr_bias, g->di_bias, g->dinitial}) ||
+        !aligned(workspace, 16))
+        return CONV2D_ERR_UNSUPPORTED;
+    const RecurPlan plan = recur_plan(prob, kRecurGradSegment);
+    if (!recur_fits(prob, plan)) return CONV2D_ERR_UNSUPPORTED;
+    const size_t need = recur_grad_bytes(prob, plan);
+    if (need && !workspace) return CONV2D_ERR_INVALID_ARGUMENT;
+    if (workspace_bytes < need) return CONV2D_ERR_WORKSPACE_TOO_SMALL;
+    RecurArgs a = recur_args(prob, plan);
+    a.x = x;
+    a.r = r;
+    a.i = i;
+    a.z = z;
+    a.dy = dy;
+    a.A = A;
+    a.r_bias = r_bias;
+    a.i_bias = i_bias;
+    a.initial = initial_state;
+    a.dfinal = dfinal;
+    a.dinitial = g->dinitial;
+    a.dx = g->dx;
+    a.dr = g->dr;
+    a.di = g->di;
+    a.dz = g->dz;
+    Carver w{(char *)workspace};
+    a.partial = w.take(up((size_t)plan.chunks * 3 * prob->d * 4));
+    a.seg_decay = w.take(plan.per_segment);
+    a.seg_state = w.take(plan.per_segment);
+    if (plan.joined) {
+        a.chunk_decay = w.take(plan.per_chunk);
+        a.chunk_state = w.take(plan.per_chunk);
+        a.back_decay = w.take(plan.per_chunk);
+        a.chunk_back = w.take(plan.per_chunk);
+    }
+    if (hipError_t h = launch_recurrence_grad(dtype, a, (hipStream_t)stream)) return status(h);
+    const ColumnSumArgs s = {a.partial, plan.chunks, 3, prob->d, {g->dA, g->dr_bias, g->di_bias}, A};
+    return status(launch_column_sums(CONV2D_DTYPE_F32, s, (hipStream_t)stream));
+}
+
+int gated_recurrence_step(const gated_recurrence_step_problem_t *p, int dtype, const void *x, const void *r, const void *i,
+                          const float *A, const void *z, const float *r_bias, const float *i_bias, float *state,
+                          const int *slots, void *y, void *stream)
+{
+    if (!p || p->rows < 0 || p->pool < 0 || p->d < 1) return CONV2D_ERR_INVALID_ARGUMENT;
+    for (long long v : {p->x_row, p->r_row, p->i_row, p->z_row})
+        if (v < 0) return CONV2D_ERR_INVALID_ARGUMENT;
+    if (!float_type(dtype) || p->d > kMaxStride) return CONV2D_ERR_UNSUPPORTED;
+    if (p->rows == 0) return CONV2D_OK;
+    if (!x || !r || !i || !A || !y || (p->pool > 0 && !state)) return CONV2D_ERR_INVALID_ARGUMENT;
+    if (!all_aligned(bytes_of(dtype), {x, r, i, z, y}) || !all_aligned(4, {A, r_bias, i_bias, state, slots}))
+        return CONV2D_ERR_UNSUPPORTED;
+    if (ceil_div(p->d, 256) > kMaxGridY || !fits(p->rows, 256)) return CONV2D_ERR_UNSUPPORTED;
+    const RecurStepArgs a = {p->rows, p->pool, p->d, p->x_row, p->r_row, p->i_row, p->z_row, x, r, i, z, A, r_bias, i_bias,
+                             state, slots, y};
+    return status(launch_recurrence_step(dtype, a, (hipStream_t)stream));
+}
+
+int layer_norm(const layer_norm_problem_t *prob, int dtype, int param_dtype, const void *x, const void *residual,
+               const void *weight, const void *bias, void *y, void *total, void *stream)
+{
+    const int e = check_norm(prob, dtype, param_dtype);
+    if (e != CONV2D_OK) return e;
+    NormArgs a = norm_args(prob, param_dtype);
+    if (a.rows == 0) return CONV2D_OK;
+    if (!x || !y) return CONV2D_ERR_INVALID_ARGUMENT;
+    if (!all_aligned(bytes_of(dtype), {x, residual, y, total}) || !all_aligned(bytes_of(param_dtype), {weight, bias}))
+        return CONV2D_ERR_UNSUPPORTED;
+    a.x = x;
+    a.residual = residual;
+    a.weight = weight;
+    a.bias = bias;
+    a.y = y;
+    a.total = total;
+    const NormShape shape = layer_norm_shape(dtype, a.rows, a.d);
+    if (!norm_fits(shape, a.rows)) return CONV2D_ERR_UNSUPPORTED;
+    return status(launch_layer_norm(dtype, a, shape, (hipStream_t)stream));
+}
+
+int layer_norm_grad_workspace_size(const layer_norm_problem_t *prob, int dtype, size_t *bytes)
+{
+    const int e = check_norm(prob, dtype, CONV2D_DTYPE_F32);
+    if (e != CONV2D_OK) return e;
+    if (!bytes) return CONV2D_ERR_INVALID_ARGUMENT;
+    const NormGradPlan plan = norm_grad_plan(prob, dtype);
+    if (!norm_fits(plan.shape, (long long)prob->seqs * prob->len)) return CONV2D_ERR_UNSUPPORTED;
+    *bytes = plan.partial + plan.stats;
+    return CONV2D_OK;
+}
+
+int layer_norm_grad(const layer_norm_problem_t *prob, int dtype, int param_dtype, const void *dy, const void *x,
+                    const void *weight, const void *dtotal, void *dx, void *dweight, void *dbias, void *workspace,
+                    size_t workspace_bytes, void *stream)
+{
+    const int e = check_norm(prob, dtype, param_dtype);
+    if (e != CONV2D_OK) return e;
+    NormArgs a = norm_args(prob, param_dtype);
+    if (a.rows > 0 && (!dy || !x || !dx)) return CONV2D_ERR_INVALID_ARGUMENT;
+    if (!all_aligned(bytes_of(dtype), {dy, x, dtotal, dx}) || !all_aligned(bytes_of(param_dtype), {weight, dweight, dbias}) ||
+        !aligned(workspace, 16))
+        return CONV2D_ERR_UNSUPPORTED;
+    const NormGradPlan plan = norm_grad_plan(prob, dtype);
+    if (!norm_fits(plan.shape, a.rows)) return CONV2D_ERR_UNSUPPORTED;
+    const size_t need = plan.partial + plan.stats;
+    if (need && !workspace) return CONV2D_ERR_INVALID_ARGUMENT;
+    if (workspace_bytes < need) return CONV2D_ERR_WORKSPACE_TOO_SMALL;
+    a.dy = dy;
+    a.x = x;
+    a.weight = weight;
+    a.dtotal = dtotal;
+    a.dx = dx;
+    a.per = plan.per;
+    a.parts = plan.parts;
+    Carver w{(char *)workspace};
+    a.partial = w.take(plan.partial);
+    a.stats = w.take(plan.stats);
+    if (a.rows > 0)
+        if (hipError_t h = launch_layer_norm_grad(dtype, a, plan.shape, (hipStream_t)stream)) return status(h);
+    if (!dweight && !dbias) return CONV2D_OK;
+    const ColumnSumArgs s = {a.partial, plan.parts, 2, prob->d, {dweight, dbias, nullptr}, nullptr};
+    return status(launch_column_sums(param_dtype, s, (hipStream_t)stream));
+}
+
+int fp4_quantize(int dtype, int m, int k, const void *x, long long x_row, void *q, long long q_pitch, void *scale,
+                 void *stream)
+{
+    if (m < 0 || k < 0 || x_row < 0) return CONV2D_ERR_INVALID_ARGUMENT;
+    const long long groups = ceil_div(k, kFp4Group);
+    if (q_pitch < groups * 16) return CONV2D_ERR_INVALID_ARGUMENT;
+    if (!float_type(dtype) || q_pitch % 16) return CONV2D_ERR_UNSUPPORTED;
+    if (m == 0 || k == 0) return CONV2D_OK;
+    if (!x || !q || !scale) return CONV2D_ERR_INVALID_ARGUMENT;
+    if (!aligned(x, bytes_of(dtype)) || !aligned(q, 16)) return CONV2D_ERR_UNSUPPORTED;
+    if (!fits(ceil_div(groups * m, 64), 256)) return CONV2D_ERR_UNSUPPORTED;
+    const Fp4QuantArgs a = {m, k, (int)groups, x_row, q_pitch, x, (uint8_t *)q, (uint8_t *)scale};
+    return status(launch_fp4_quantize(dtype, a, (hipStream_t)stream));
+}
+
+int fp4_matmul(const fp4_matmul_problem_t *p, int dtype, const void *x, const void *w, const void *w_scale, void *out,
+               void *stream)
+{
+    if (!p || p->m < 0 || p->n < 0 || p->k < 0 || p->x_row < 0) return CONV2D_ERR_INVALID_ARGUMENT;
+    const long long groups = ceil_div(p->k, kFp4Group);
+    if (p->w_pitch < groups * 16) return CONV2D_ERR_INVALID_ARGUMENT;
+    if (!float_type(dtype) || p->w_pitch % 16) return CONV2D_ERR_UNSUPPORTED;
+    if (p->m == 0 || p->n == 0) return CONV2D_OK;
+    if (!out || (p->k > 0 && (!x || !w || !w_scale))) return CONV2D_ERR_INVALID_ARGUMENT;
+    if (!all_aligned(bytes_of(dtype), {x, out}) || !aligned(w, 16)) return CONV2D_ERR_UNSUPPORTED;
+    if (ceil_div(p->m, 64) > kMaxGridY || !fits(ceil_div(p->n, 16), 512)) return CONV2D_ERR_UNSUPPORTED;
+    const Fp4MatmulArgs a = {p->m, p->n, p->k, (int)groups, p->x_row, p->w_pitch, x, (const uint8_t *)w,
+                             (const uint8_t *)w_scale, out};
+    return status(launch_fp4_matmul(dtype, a, (hipStream_t)stream));
+}
+
+}  // extern "C"

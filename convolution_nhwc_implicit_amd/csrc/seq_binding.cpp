@@ -577,9 +577,283 @@ PyObject *py_fp8_matmul(PyObject *, PyObject *const *a, Py_ssize_t n)
     END_HANDLE_TH_ERRORS
 }
 
+// ---------------------------------------------------------------- gated recurrence
+struct Recur {
+    Checks c;
+    const Tensor *x, *r, *i, *A, *z, *r_bias, *i_bias;
+    int code;
+    int64_t d;
+    // x, r, i, A, z, r_bias, i_bias
+    Recur(PyObject *const *a)
+    {
+        x = tensor(a[0], "x");
+        r = tensor(a[1], "r");
+        i = tensor(a[2], "i");
+        A = tensor(a[3], "A");
+        z = maybe(a[4], "z");
+        r_bias = maybe(a[5], "r_bias");
+        i_bias = maybe(a[6], "i_bias");
+        code = float_code(*x, "x");
+        const at::ScalarType type = x->scalar_type();
+        if (x->dim() < 2) value_error("x must be [tokens][d] or [sequences][tokens][d]");
+        d = x->size(-1);
+        c.strided(*x, "x", type, x->sizes());
+        c.strided(*r, "r", type, x->sizes());
+        c.strided(*i, "i", type, x->sizes());
+        if (z) c.strided(*z, "z", type, x->sizes());
+        c.dense(A, "A", at::kFloat, {d});
+        c.dense(r_bias, "r_bias", at::kFloat, {d});
+        c.dense(i_bias, "i_bias", at::kFloat, {d});
+    }
+    static const float *f(const Tensor *t) { return (const float *)ptr(t); }
+};
+
+struct RecurTokens : Recur {
+    const Tensor *initial;
+    gated_recurrence_problem_t p;
+    int64_t seqs;
+    // x .. i_bias, initial_state, seq_start
+    RecurTokens(PyObject *const *a) : Recur(a)
+    {
+        initial = maybe(a[7], "initial_state");
+        const Lead lead(*x, maybe(a[8], "seq_start"), c);
+        seqs = lead.seqs;
+        c.dense(initial, "initial_state", at::kFloat, {seqs, d});
+        p = {lead.batch, int_size(d, "d"), lead.strides(*x), lead.strides(*r), lead.strides(*i),
+             z ? lead.strides(*z) : seq_stride_t{0, 0}, {0, 0}};
+    }
+};
+
+PyObject *py_gated_recurrence(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    expect_args(n, 10);
+    RecurTokens v(a);
+    const bool state = truth(a[9]);
+    v.c.device(*v.x);
+    v.c.detached("gated_recurrence", "gated_recurrence_grad computes the gradients");
+    const c10::DeviceGuard guard(v.x->device());
+    size_t need = 0;
+    raise(gated_recurrence_workspace_size(&v.p, v.code, &need), "gated_recurrence_workspace_size");
+    const Tensor y = new_tensor(*v.x, v.x->sizes(), v.x->scalar_type());
+    const Tensor s = state ? new_tensor(*v.x, {v.seqs, v.d}, at::kFloat) : Tensor();
+    const Tensor ws = workspace(*v.x, need);
+    raise(gated_recurrence(&v.p, v.code, ptr(v.x), ptr(v.r), ptr(v.i), v.f(v.A), ptr(v.z), v.f(v.r_bias), v.f(v.i_bias),
+                           v.f(v.initial), out_ptr(y), (float *)out_ptr(s), out_ptr(ws), need, stream_of(*v.x)),
+          "gated_recurrence");
+    return state ? pair(y, s) : wrap(y);
+    END_HANDLE_TH_ERRORS
+}
+
+PyObject *py_gated_recurrence_grad(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    expect_args(n, 11);
+    const Tensor *dy = tensor(a[0], "dy");
+    RecurTokens v(a + 1);
+    const Tensor *dfinal = maybe(a[10], "dfinal_state");
+    v.c.strided(*dy, "dy", v.x->scalar_type(), v.x->sizes());
+    v.c.dense(dfinal, "dfinal_state", at::kFloat, {v.seqs, v.d});
+    const size_t lead = v.x->dim() - 1;
+    v.p.dy = {dy->size(lead - 1) > 1 ? dy->stride(lead - 1) : 0, lead == 2 && dy->size(0) > 1 ? dy->stride(0) : 0};
+    v.c.device(*v.x);
+    const c10::DeviceGuard guard(v.x->device());
+    size_t need = 0;
+    raise(gated_recurrence_grad_workspace_size(&v.p, v.code, &need), "gated_recurrence_grad_workspace_size");
+    auto like = [&](const Tensor *t) { return t ? new_tensor(*v.x, t->sizes(), t->scalar_type()) : Tensor(); };
+    const Tensor dx = like(v.x), dr = like(v.r), di = like(v.i), dA = like(v.A), dz = like(v.z);
+    const Tensor drb = like(v.r_bias), dib = like(v.i_bias), d0 = like(v.initial);
+    const Tensor ws = workspace(*v.x, need);
+    const gated_recurrence_grads_t g = {out_ptr(dx), out_ptr(dr), out_ptr(di), (float *)out_ptr(dA), out_ptr(dz),
+                                        (float *)out_ptr(drb), (float *)out_ptr(dib), (float *)out_ptr(d0)};
+    raise(gated_recurrence_grad(&v.p, v.code, ptr(dy), ptr(v.x), ptr(v.r), ptr(v.i), v.f(v.A), ptr(v.z), v.f(v.r_bias),
+                                v.f(v.i_bias), v.f(v.initial), v.f(dfinal), &g, out_ptr(ws), need, stream_of(*v.x)),
+          "gated_recurrence_grad");
+    PyObject *r = PyDict_New();
+    if (!r) throw python_error();
+    set_item(r, "dx", dx);
+    set_item(r, "dr", dr);
+    set_item(r, "di", di);
+    set_item(r, "dA", dA);
+    set_item(r, "dz", dz);
+    set_item(r, "dr_bias", drb);
+    set_item(r, "di_bias", dib);
+    set_item(r, "dinitial_state", d0);
+    return r;
+    END_HANDLE_TH_ERRORS
+}
+
+PyObject *py_gated_recurrence_step(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    expect_args(n, 9);
+    Recur v(a);  // x, r, i, A, z, r_bias, i_bias, then state, slots
+    const Tensor *state = tensor(a[7], "state"), *slots = maybe(a[8], "slots");
+    if (v.x->dim() != 2 || state->dim() != 2) value_error("x must be [rows][d] and state [pool][d]");
+    const int64_t rows = v.x->size(0), pool = state->size(0);
+    v.c.dense(state, "state", at::kFloat, {pool, v.d});
+    const int *sp = slots_of(slots, rows, pool, v.c);
+    const gated_recurrence_step_problem_t p = {int_size(rows, "rows"), int_size(pool, "pool"), int_size(v.d, "d"),
+                                               row_stride(*v.x), row_stride(*v.r), row_stride(*v.i), v.z ? row_stride(*v.z) : 0};
+    v.c.device(*v.x);
+    v.c.detached("gated_recurrence_step", "gated_recurrence and gated_recurrence_grad compute prompts and their gradients");
+    const c10::DeviceGuard guard(v.x->device());
+    const Tensor y = new_tensor(*v.x, {rows, v.d}, v.x->scalar_type());
+    raise(gated_recurrence_step(&p, v.code, ptr(v.x), ptr(v.r), ptr(v.i), v.f(v.A), ptr(v.z), v.f(v.r_bias), v.f(v.i_bias),
+                                (float *)state->data_ptr(), sp, out_ptr(y), stream_of(*v.x)), "gated_recurrence_step");
+    written(*state);
+    return wrap(y);
+    END_HANDLE_TH_ERRORS
+}
+
+// ---------------------------------------------------------------------- layer norm
+struct Norm {
+    Checks c;
+    const Tensor *x, *weight, *bias;
+    int code, param_code;
+    at::ScalarType param_type;
+    int64_t d;
+    layer_norm_problem_t p;
+    Norm(PyObject *xo, PyObject *wo, PyObject *bo, PyObject *eps)
+    {
+        x = tensor(xo, "x");
+        weight = maybe(wo, "weight");
+        bias = maybe(bo, "bias");
+        code = float_code(*x, "x");
+        const double e = PyFloat_AsDouble(eps);
+        if (e == -1.0 && PyErr_Occurred()) throw python_error();
+        if (!(e >= 0.0) || !((float)e <= 3.402823466e38f)) value_error("eps must be finite and not negative");
+        if (x->dim() < 2 || x->dim() > 3) value_error("x must be [tokens][d] or [sequences][tokens][d]");
+        d = x->size(-1);
+        if (d < 1) value_error("rows must have at least one element");
+        c.strided(*x, "x", x->scalar_type(), x->sizes());
+        const Tensor *first = weight ? weight : bias;
+        param_type = first && first->scalar_type() == at::kFloat ? at::kFloat : x->scalar_type();
+        param_code = param_type == at::kFloat ? CONV2D_DTYPE_F32 : code;
+        c.dense(weight, "weight", param_type, {d});
+        c.dense(bias, "bias", param_type, {d});
+        const size_t n = x->dim();
+        const int64_t seqs = n == 3 ? x->size(0) : 1, len = x->size(n - 2);
+        p = {int_size(seqs, "sequences"), int_size(len, "tokens"), int_size(d, "d"), (float)e, strides(*x), {0, 0}, {0, 0}, {0, 0}};
+        // rows that one stride reaches need no sequences
+        if (seqs * len > INT32_MAX) value_error("there are at most 2^31 - 1 rows");
+    }
+    seq_stride_t strides(const Tensor &t) const
+    {
+        const size_t n = t.dim();
+        return {t.size(n - 2) > 1 ? t.stride(n - 2) : 0, n == 3 && t.size(0) > 1 ? t.stride(0) : 0};
+    }
+};
+
+PyObject *py_layer_norm(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    expect_args(n, 5);
+    Norm v(a[0], a[1], a[2], a[3]);
+    const Tensor *residual = maybe(a[4], "residual");
+    const at::ScalarType type = v.x->scalar_type();
+    if (residual) {
+        v.c.strided(*residual, "residual", type, v.x->sizes());
+        v.p.residual = v.strides(*residual);
+    }
+    v.c.device(*v.x);
+    v.c.detached("layer_norm", "layer_norm_grad computes the gradients");
+    const c10::DeviceGuard guard(v.x->device());
+    const Tensor y = new_tensor(*v.x, v.x->sizes(), type), total = residual ? new_tensor(*v.x, v.x->sizes(), type) : Tensor();
+    raise(layer_norm(&v.p, v.code, v.param_code, ptr(v.x), ptr(residual), ptr(v.weight), ptr(v.bias), out_ptr(y),
+                     out_ptr(total), stream_of(*v.x)), "layer_norm");
+    return residual ? pair(y, total) : wrap(y);
+    END_HANDLE_TH_ERRORS
+}
+
+PyObject *py_layer_norm_grad(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    expect_args(n, 6);
+    const Tensor *dy = tensor(a[0], "dy");
+    Norm v(a[1], a[2], a[3], a[4]);
+    const Tensor *dtotal = maybe(a[5], "dtotal");
+    const at::ScalarType type = v.x->scalar_type();
+    v.c.strided(*dy, "dy", type, v.x->sizes());
+    v.p.dy = v.strides(*dy);
+    if (dtotal) {
+        v.c.strided(*dtotal, "dtotal", type, v.x->sizes());
+        v.p.dtotal = v.strides(*dtotal);
+    }
+    v.c.device(*v.x);
+    const c10::DeviceGuard guard(v.x->device());
+    size_t need = 0;
+    raise(layer_norm_grad_workspace_size(&v.p, v.code, &need), "layer_norm_grad_workspace_size");
+    const Tensor dx = new_tensor(*v.x, v.x->sizes(), type);
+    const Tensor dw = v.weight ? new_tensor(*v.x, {v.d}, v.param_type) : Tensor();
+    const Tensor db = v.bias ? new_tensor(*v.x, {v.d}, v.param_type) : Tensor();
+    const Tensor ws = workspace(*v.x, need);
+    raise(layer_norm_grad(&v.p, v.code, v.param_code, ptr(dy), ptr(v.x), ptr(v.weight), ptr(dtotal), out_ptr(dx),
+                          out_ptr(dw), out_ptr(db), out_ptr(ws), need, stream_of(*v.x)), "layer_norm_grad");
+    PyObject *r = PyDict_New();
+    if (!r) throw python_error();
+    set_item(r, "dx", dx);
+    set_item(r, "dw", dw);
+    set_item(r, "db", db);
+    return r;
+    END_HANDLE_TH_ERRORS
+}
+
+// ------------------------------------------------------------------ 4-bit products
+int64_t fp4_groups(int64_t k) { return (k + 31) / 32; }
+
+PyObject *py_fp4_quantize(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    expect_args(n, 1);
+    const Tensor *x = tensor(a[0], "x");
+    const int code = float_code(*x, "x");
+    if (x->dim() != 2) value_error("x must be [m][k]");
+    Checks c;
+    c.strided(*x, "x", x->scalar_type(), x->sizes());
+    c.device(*x);
+    c.detached("fp4_quantize", "rounding to 4 bits has none");
+    const int64_t m = x->size(0), k = x->size(1), pitch = fp4_groups(k) * 16, cols = (k + 1) / 2;
+    const c10::DeviceGuard guard(x->device());
+    const Tensor q = new_tensor(*x, {m, pitch}, at::kByte), scale = new_tensor(*x, {m, fp4_groups(k)}, at::kByte);
+    raise(fp4_quantize(code, int_size(m, "m"), int_size(k, "k"), ptr(x), row_stride(*x), out_ptr(q), pitch, out_ptr(scale),
+                       stream_of(*x)), "fp4_quantize");
+    return pair(pitch == cols ? q : q.narrow(1, 0, cols), scale);
+    END_HANDLE_TH_ERRORS
+}
+
+PyObject *py_fp4_matmul(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    expect_args(n, 3);
+    const Tensor *x = tensor(a[0], "x"), *w = tensor(a[1], "w"), *ws = tensor(a[2], "w_scale");
+    const int code = float_code(*x, "x");
+    if (x->dim() != 2 || w->dim() != 2) value_error("x must be [m][k] and w [n][ceil(k/2)]");
+    Checks c;
+    const int64_t m = x->size(0), k = x->size(1), rows = w->size(0), groups = fp4_groups(k);
+    c.strided(*x, "x", x->scalar_type(), x->sizes());
+    c.strided(*w, "w", at::kByte, {rows, (k + 1) / 2});
+    c.dense(ws, "w_scale", at::kByte, {rows, groups});
+    const int64_t pitch = rows > 1 && k > 0 ? w->stride(0) : groups * 16;
+    // whole groups are read: the last row's too has to lie in w's memory to its last group's end
+    if (pitch % 16 || pitch < groups * 16 ||
+        (rows > 0 && k > 0 && (w->storage_offset() + (rows - 1) * pitch + groups * 16) > (int64_t)w->storage().nbytes()))
+        value_error("w's rows must start on 16-byte steps and hold whole groups of 32 values (fp4_quantize lays them out so)");
+    c.device(*x);
+    c.detached("fp4_matmul", "quantised weights have none");
+    const fp4_matmul_problem_t p = {int_size(m, "m"), int_size(rows, "n"), int_size(k, "k"), row_stride(*x), pitch};
+    const c10::DeviceGuard guard(x->device());
+    const Tensor out = new_tensor(*x, {m, rows}, x->scalar_type());
+    raise(fp4_matmul(&p, code, ptr(x), ptr(w), ptr(ws), out_ptr(out), stream_of(*x)), "fp4_matmul");
+    return wrap(out);
+    END_HANDLE_TH_ERRORS
+}
+
 #define FN(name) {#name, (PyCFunction)(void (*)(void))py_##name, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FN(causal_conv), FN(causal_conv_grad), FN(causal_conv_step), FN(selective_scan),
                          FN(selective_scan_grad), FN(selective_scan_step), FN(fp8_quantize), FN(fp8_matmul),
+                         FN(gated_recurrence), FN(gated_recurrence_grad), FN(gated_recurrence_step), FN(layer_norm),
+                         FN(layer_norm_grad), FN(fp4_quantize), FN(fp4_matmul),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_sequence", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

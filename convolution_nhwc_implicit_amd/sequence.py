@@ -1,8 +1,10 @@
 """The sequence operators on torch tensors.
 
-``causal_conv`` and ``selective_scan`` with their gradients (``*_grad``) and
-their single-token forms on pooled states (``*_step``), and the block-scaled
-fp8 products (``fp8_quantize``, ``fp8_matmul``).  The native module _sequence
+``causal_conv``, ``selective_scan`` and ``gated_recurrence`` with their gradients
+(``*_grad``) and their single-token forms on pooled states (``*_step``),
+``layer_norm`` with its gradients, the block-scaled fp8 products
+(``fp8_quantize``, ``fp8_matmul``) and products with 4-bit weights
+(``fp4_quantize``, ``fp4_matmul``).  The native module _sequence
 checks the arguments, allocates outputs and workspaces on the current stream
 and calls the C ABI in include/sequence_ops.h; the computation runs in the HIP
 kernels of libconv2d_nhwc.so.  The step forms write their states in place.
@@ -102,6 +104,49 @@ def selective_scan_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, sof
     return load().selective_scan_step(x, dt, A, B, C, D, z, dt_bias, state, softplus, slots)
 
 
+# -------------------------------------------------------------- gated recurrence
+
+def gated_recurrence(x, r, i, A, z=None, r_bias=None, i_bias=None, initial_state=None, seq_start=None,
+                     return_state=False):
+    """a = exp(A sigmoid(r + r_bias));  h = a h + sqrt(1 - a^2) sigmoid(i + i_bias) x;  y = h silu(z) (without z: h),
+    token after token and channel by channel.
+
+    x, r, i, z [..][d] in one type; A (log decays, at most 0), r_bias, i_bias [d] and the states [seqs][d] in float32.
+    Positive A gives NaN; rates below -2e38 count as -2e38. With return_state the result is (y, final_state)."""
+    return load().gated_recurrence(x, r, i, A, z, r_bias, i_bias, initial_state, seq_start, return_state)
+
+
+def gated_recurrence_grad(dy, x, r, i, A, z=None, r_bias=None, i_bias=None, initial_state=None, seq_start=None,
+                          dfinal_state=None):
+    """Gradients of gated_recurrence for the output gradient dy (and that of the returned state, if given): a dict of
+    dx, dr, di, dz in x's type and dA, dr_bias, di_bias, dinitial_state in float32; None where the input is None.
+    The forward pass is computed again, not kept. dA is 0 where A is 0 (the square root has no derivative there)."""
+    return load().gated_recurrence_grad(dy, x, r, i, A, z, r_bias, i_bias, initial_state, seq_start, dfinal_state)
+
+
+def gated_recurrence_step(x, r, i, A, state, z=None, r_bias=None, i_bias=None, slots=None):
+    """gated_recurrence for one token per request: x, r, i, z [rows][d], state [pool][d] float32 (updated in place),
+    slots as for causal_conv_step."""
+    return load().gated_recurrence_step(x, r, i, A, z, r_bias, i_bias, state, slots)
+
+
+# -------------------------------------------------------------------- layer norm
+
+def layer_norm(x, weight=None, bias=None, eps=1e-5, residual=None):
+    """y = (t - mean) / sqrt(var + eps) * weight + bias over the last axis, of t = x, or of t = x + residual: then the
+    result is (y, total) with total = t in x's type. y comes from the unrounded sum, statistics are float32.
+
+    x, residual [tokens][d] or [sequences][tokens][d]; weight and bias [d] in x's type or both in float32."""
+    return load().layer_norm(x, weight, bias, eps, residual)
+
+
+def layer_norm_grad(dy, x, weight=None, bias=None, eps=1e-5, dtotal=None):
+    """Gradients of layer_norm at t = x (its total, where there was a residual) for the output gradient dy: a dict of
+    dx in x's type (also the residual's gradient; dtotal, the gradient that reaches total on other ways, is added to
+    it) and dw, db in the parameters' type (None where the parameter is None)."""
+    return load().layer_norm_grad(dy, x, weight, bias, eps, dtotal)
+
+
 # ------------------------------------------------------------ block-scaled fp8 products
 
 def fp8_quantize(x, transpose=False, blocks=False):
@@ -123,3 +168,21 @@ def fp8_matmul(a, a_scale, b, b_scale, out_dtype=torch.bfloat16):
     cuts each group of 8 neighbouring products at 2^-13 of its largest, below the result's own rounding (a float32
     result has no such cut, and may be rounded afterwards)."""
     return load().fp8_matmul(a, a_scale, b, b_scale, out_dtype)
+
+
+# ---------------------------------------------------------------- 4-bit products
+
+def fp4_quantize(x):
+    """x [m][k] to e2m1 values with a power-of-two scale for every 32 values of a row: (q [m][ceil(k/2)], scale
+    [m][ceil(k/32)]), both uint8. Byte j of a row of q holds values 2j (low half) and 2j + 1; a scale byte e stands for
+    2^(e - 127). Scales are the least that bring a group's values into e2m1's range; a group with an infinity or a NaN
+    becomes NaN (e = 255). q's rows are padded with zeros to whole groups; q is a view of them."""
+    return load().fp4_quantize(x)
+
+
+def fp4_matmul(x, w, w_scale):
+    """x times w's transpose: out [m][n] in x's type, of x [m][k] in float16, bfloat16 or float32 and 4-bit w (as
+    fp4_quantize makes it: [n][ceil(k/2)], w_scale [n][ceil(k/32)]). Products are exact, sums float32, rounded once.
+    Made for few rows of x (new tokens), where the weights' bytes are what there is to do; for many rows fp8_matmul is
+    faster."""
+    return load().fp4_matmul(x, w, w_scale)

@@ -1,7 +1,8 @@
 /*
  * sequence_ops.h -- C ABI of the sequence operators of the MI355X (gfx950)
- * library: the causal convolution and the selective scan of a gated state
- * space block, and block-scaled fp8 matrix products.
+ * library: the causal convolution, the selective scan and the gated recurrence
+ * of recurrent blocks, the layer norm in front of them, and matrix products of
+ * block-scaled fp8 and of 4-bit weights.
  *
  * Conventions (as conv2d_nhwc.h where not stated otherwise):
  *   - The caller owns every buffer; the library allocates nothing.  Work is
@@ -238,6 +239,137 @@ int fp8_matmul_workspace_size(const fp8_matmul_problem_t *prob, int dtype, size_
 int fp8_matmul(const fp8_matmul_problem_t *prob, int dtype, const void *a, const float *a_scale,
                const void *b, const float *b_scale, void *out, void *workspace, size_t workspace_bytes,
                void *stream);
+
+/*
+ * Gated linear recurrence, channel by channel:
+ *   g = sigmoid(r[t][c] + r_bias[c]);  u = sigmoid(i[t][c] + i_bias[c])
+ *   a = exp(A[c] * g);  h[t][c] = a * h[t-1][c] + sqrt(1 - a^2) * u * x[t][c]
+ *   y[t][c] = h[t][c] * silu(z[t][c])
+ * with h before a sequence's first token its initial_state, or zero without one.
+ *   x, r, i, z  rows of d elements, dtype, with the strides below.  z may be NULL
+ *             (y = h).
+ *   A [d] (log decays, at most 0: growing states are NaN; rates below -2e38 count
+ *             as -2e38), r_bias, i_bias [d] (may be NULL: zero), initial_state and
+ *             final_state [seqs][d] (may be NULL): fp32, dense.  The states must
+ *             not overlap.
+ *   y [tokens][d] dense, dtype; must not overlap the inputs
+ * Decays are also multiplied over runs of tokens before they meet a state: an
+ * infinite state is NaN where such a product is 0.  Gates below 2^-126 count as 0.
+ * Row strides and d are below 2^24.  Long sequences are cut into chunks that run
+ * side by side, joined through the workspace (16-byte aligned; its size may be 0).
+ */
+typedef struct gated_recurrence_problem {
+    seq_batch_t batch;
+    int d;
+    seq_stride_t x, r, i, z, dy;
+} gated_recurrence_problem_t;
+
+int gated_recurrence_workspace_size(const gated_recurrence_problem_t *prob, int dtype, size_t *bytes);
+int gated_recurrence(const gated_recurrence_problem_t *prob, int dtype, const void *x, const void *r,
+                     const void *i, const float *A, const void *z, const float *r_bias,
+                     const float *i_bias, const float *initial_state, void *y, float *final_state,
+                     void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Gradients of gated_recurrence for the output gradient dy (strides `dy`) and, if
+ * given, that of final_state.  The forward pass's states are computed again.
+ *   dx, dr, di, dz [tokens][d] (dz only with z): dtype, dense; dA [d], dr_bias and
+ *   di_bias [d] (NULL if not wanted), dinitial [seqs][d] (likewise): fp32.
+ * All are overwritten; nothing may overlap an input.  The sums run over the rows
+ * that sequences cover.  dA is 0 where A is 0, where the square root has no
+ * derivative.
+ */
+typedef struct gated_recurrence_grads {
+    void *dx, *dr, *di;
+    float *dA;
+    void *dz;
+    float *dr_bias, *di_bias, *dinitial;
+} gated_recurrence_grads_t;
+
+int gated_recurrence_grad_workspace_size(const gated_recurrence_problem_t *prob, int dtype, size_t *bytes);
+int gated_recurrence_grad(const gated_recurrence_problem_t *prob, int dtype, const void *dy, const void *x,
+                          const void *r, const void *i, const float *A, const void *z, const float *r_bias,
+                          const float *i_bias, const float *initial_state, const float *dfinal,
+                          const gated_recurrence_grads_t *grads, void *workspace, size_t workspace_bytes,
+                          void *stream);
+
+/*
+ * gated_recurrence for one new token per request, on fp32 states [pool][d]
+ * updated in place; slots as for causal_conv_step.  The tensors' rows are
+ * requests, with the strides given.
+ */
+typedef struct gated_recurrence_step_problem {
+    int rows, pool, d;
+    long long x_row, r_row, i_row, z_row;
+} gated_recurrence_step_problem_t;
+
+int gated_recurrence_step(const gated_recurrence_step_problem_t *prob, int dtype, const void *x, const void *r,
+                          const void *i, const float *A, const void *z, const float *r_bias,
+                          const float *i_bias, float *state, const int *slots, void *y, void *stream);
+
+/*
+ * Layer norm of rows of d elements, with the residual sum in front of it:
+ *   t = x + residual (or x);  y = (t - mean(t)) / sqrt(var(t) + eps) * weight + bias
+ * with the mean and the variance (of d elements, two-pass) of the unrounded fp32 sum.
+ *   x, residual  dtype, strides below.  residual may be NULL.
+ *   weight, bias [d], param_dtype (dtype or CONV2D_DTYPE_F32); NULL = one, zero
+ *   y, total     [rows][d] dense, dtype; total receives t, rounded, and may be NULL.
+ *                They must not overlap the inputs or each other.
+ * rows = seqs * len, in sequences only for their strides; 0 <= eps, finite.
+ */
+typedef struct layer_norm_problem {
+    int seqs, len; /* rows: [seqs][len] */
+    int d;
+    float eps;
+    seq_stride_t x, residual, dy, dtotal;
+} layer_norm_problem_t;
+
+int layer_norm(const layer_norm_problem_t *prob, int dtype, int param_dtype, const void *x,
+               const void *residual, const void *weight, const void *bias, void *y, void *total,
+               void *stream);
+
+/*
+ * Gradients of layer_norm at t = x (its `total`, where there is one) for the output
+ * gradient dy and, if given, that of total (which is added to dx).
+ *   dx [rows][d] dtype, dense; dweight, dbias [d] param_dtype (NULL if not wanted).
+ * The workspace (16-byte aligned) holds fp32 partial sums over runs of rows.
+ */
+int layer_norm_grad_workspace_size(const layer_norm_problem_t *prob, int dtype, size_t *bytes);
+int layer_norm_grad(const layer_norm_problem_t *prob, int dtype, int param_dtype, const void *dy,
+                    const void *x, const void *weight, const void *dtotal, void *dx, void *dweight,
+                    void *dbias, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * 4-bit operands: e2m1 values (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives), two
+ * to a byte with the even one in the low half, and for every 32 values of a row one
+ * byte e that scales them by 2^(e - 127); e = 255 makes them NaN.
+ *
+ * fp4_quantize: x [m][k] (dtype, row stride x_row, in elements) to such an operand,
+ * q [m][q_pitch] bytes and scale [m][ceil(k/32)].  The scale is the least power of
+ * two, at least 2^-127, that brings its values into e2m1's range; values go to the
+ * nearest, ties to the even one.  A group with an infinity or a NaN gets e = 255.
+ * q_pitch is a multiple of 16, at least 16 * ceil(k/32); q is 16-byte aligned.
+ * Bytes past a row's groups are left alone, and those past its values are zero.
+ */
+int fp4_quantize(int dtype, int m, int k, const void *x, long long x_row, void *q, long long q_pitch,
+                 void *scale, void *stream);
+
+/*
+ * out[i][j] = sum_k x[i][k] * w[j][k] for 4-bit w: exact products, fp32 sums, one
+ * rounding to dtype (CONV2D_DTYPE_F16, _BF16 or _F32: x's type too).  Made for few
+ * rows of x, where the weights' bytes are what there is to do.
+ *   x [m][k], row stride x_row; w [n][w_pitch] bytes, 16-byte aligned, w_pitch a
+ *   multiple of 16, at least 16 * ceil(k/32); w_scale [n][ceil(k/32)]; out [m][n]
+ *   dense; must not overlap the operands.
+ * Halves of bytes past k are read but have no influence.
+ */
+typedef struct fp4_matmul_problem {
+    int m, n, k;
+    long long x_row, w_pitch;
+} fp4_matmul_problem_t;
+
+int fp4_matmul(const fp4_matmul_problem_t *prob, int dtype, const void *x, const void *w,
+               const void *w_scale, void *out, void *stream);
 
 #ifdef __cplusplus
 }
