@@ -27,26 +27,32 @@ int check_recurrence(const gated_recurrence_problem_t *p, int dtype, bool grad)
 }
 
 struct RecurPlan {
-    int chunk, chunks, joined;
+    int chunk, chunks, joined, per_seq;
     size_t per_chunk, per_segment;  // bytes of a value for each of them and channel
 };
 
+// Whether one stride reaches all rows of a batch.
+bool one_stride(const seq_batch_t &b, const seq_stride_t &s) { return b.seq_start || b.seqs == 1 || s.seq == b.len * s.row; }
+
 // Tokens of a chunk: sequences stay whole where that alone fills the chip (a workgroup
 // to a compute unit), since cut ones are read twice; else about two workgroups to each.
-RecurPlan recur_plan(const gated_recurrence_problem_t *p, int segment)
+// Chunks run over all tokens, sequences' borders inside them, unless a dense batch's
+// sequences lie apart.
+RecurPlan recur_plan(const gated_recurrence_problem_t *p, int segment, bool grad)
 {
     const seq_batch_t &b = p->batch;
-    const long long across = ceil_div(p->d, kRecurChannels);
-    long long chunk;
-    if (!b.seq_start && b.len > 0 && b.len % segment == 0 && b.len <= kRecurChunkMost && across * b.seqs >= kCUs)
-        chunk = b.len;
-    else
-        chunk = ceil_div(ceil_div(b.tokens, ceil_div(2 * kCUs, across)), segment) * segment;
-    chunk = std::min<long long>(std::max<long long>(chunk, segment), kRecurChunkMost);
+    bool flat = one_stride(b, p->x) && one_stride(b, p->r) && one_stride(b, p->i) && one_stride(b, p->z);
+    if (grad) flat = flat && one_stride(b, p->dy);
+    const long long across = ceil_div(p->d, kRecurChannels), pieces = ceil_div(2 * kCUs, across);
+    const long long most = flat ? b.tokens : b.len;  // tokens that a chunk can have
+    long long chunk = ceil_div(ceil_div(b.tokens, pieces), segment) * segment;
+    if (!b.seq_start && b.len > 0 && b.len % segment == 0 && across * b.seqs >= kCUs) chunk = b.len;
+    chunk = std::min(std::min<long long>(std::max<long long>(chunk, segment), kRecurChunkMost), std::max(1LL, ceil_div(most, segment)) * segment);
     RecurPlan r;
     r.chunk = (int)chunk;
-    r.chunks = (int)ceil_div(b.tokens, chunk);
-    r.joined = r.chunks > 1 && (b.seq_start || chunk % b.len != 0);
+    r.per_seq = flat ? 0 : (int)ceil_div(b.len, chunk);
+    r.chunks = flat ? (int)ceil_div(b.tokens, chunk) : r.per_seq * b.seqs;
+    r.joined = flat ? r.chunks > 1 && (b.seq_start || chunk % b.len != 0) : r.per_seq > 1;
     r.per_chunk = up((size_t)r.chunks * p->d * 4);
     r.per_segment = up((size_t)r.chunks * (chunk / segment) * p->d * 4);
     return r;
@@ -70,6 +76,7 @@ RecurArgs recur_args(const gated_recurrence_problem_t *p, const RecurPlan &r)
     a.chunk = r.chunk;
     a.chunks = r.chunks;
     a.joined = r.joined;
+    a.per_seq = r.per_seq;
     a.xs = stride_of(p->x);
     a.rs = stride_of(p->r);
     a.is = stride_of(p->i);
@@ -137,7 +144,7 @@ int gated_recurrence_workspace_size(const gated_recurrence_problem_t *prob, int 
     const int r = check_recurrence(prob, dtype, false);
     if (r != CONV2D_OK) return r;
     if (!bytes) return CONV2D_ERR_INVALID_ARGUMENT;
-    const RecurPlan plan = recur_plan(prob, kRecurSegment);
+    const RecurPlan plan = recur_plan(prob, kRecurSegment, false);
     if (!recur_fits(prob, plan)) return CONV2D_ERR_UNSUPPORTED;
     *bytes = recur_bytes(plan);
     return CONV2D_OK;
@@ -154,7 +161,7 @@ int gated_recurrence(const gated_recurrence_problem_t *prob, int dtype, const vo
     if (!all_aligned(bytes_of(dtype), {x, r, i, z, y}) || !all_aligned(4, {A, r_bias, i_bias, initial_state, final_state}) ||
         !aligned(workspace, 16))
         return CONV2D_ERR_UNSUPPORTED;
-    const RecurPlan plan = recur_plan(prob, kRecurSegment);
+    const RecurPlan plan = recur_plan(prob, kRecurSegment, false);
     if (!recur_fits(prob, plan)) return CONV2D_ERR_UNSUPPORTED;
     const size_t need = recur_bytes(plan);
     if (need && !workspace) return CONV2D_ERR_INVALID_ARGUMENT;
@@ -184,7 +191,7 @@ int gated_recurrence_grad_workspace_size(const gated_recurrence_problem_t *prob,
     const int r = check_recurrence(prob, dtype, true);
     if (r != CONV2D_OK) return r;
     if (!bytes) return CONV2D_ERR_INVALID_ARGUMENT;
-    const RecurPlan plan = recur_plan(prob, kRecurGradSegment);
+    const RecurPlan plan = recur_plan(prob, kRecurGradSegment, true);
     if (!recur_fits(prob, plan)) return CONV2D_ERR_UNSUPPORTED;
     *bytes = recur_grad_bytes(prob, plan);
     return CONV2D_OK;
@@ -204,7 +211,7 @@ int gated_recurrence_grad(const gated_recurrence_problem_t *prob, int dtype, con
         !all_aligned(4, {A, r_bias, i_bias, initial_state, dfinal, g->dA, g->dr_bias, g->di_bias, g->dinitial}) ||
         !aligned(workspace, 16))
         return CONV2D_ERR_UNSUPPORTED;
-    const RecurPlan plan = recur_plan(prob, kRecurGradSegment);
+    const RecurPlan plan = recur_plan(prob, kRecurGradSegment, true);
     if (!recur_fits(prob, plan)) return CONV2D_ERR_UNSUPPORTED;
     const size_t need = recur_grad_bytes(prob, plan);
     if (need && !workspace) return CONV2D_ERR_INVALID_ARGUMENT;

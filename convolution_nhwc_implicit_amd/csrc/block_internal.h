@@ -58,6 +58,7 @@ struct RecurArgs {
     int d;
     int chunk, chunks;   // tokens of a chunk (whole segments), chunks in all
     int joined;          // chunks start inside sequences
+    int per_seq;         // chunks of each sequence; 0: chunks run over all tokens
     RowStride xs, rs, is, zs, dys;
     const void *x, *r, *i, *z, *dy;
     const float *A, *r_bias, *i_bias, *initial, *dfinal;
@@ -79,7 +80,7 @@ struct RecurStepArgs {
     const int *slots;
     void *y;
 };
-constexpr int kRecurRun = 16, kRecurWaves = 8;          // forward: tokens of a wave's run, waves of a workgroup
+constexpr int kRecurRun = 8, kRecurWaves = 8;          // forward: tokens of a wave's run, waves of a workgroup
 constexpr int kRecurGradRun = 8, kRecurGradWaves = 8;   // gradient
 constexpr int kRecurSegment = kRecurRun * kRecurWaves, kRecurGradSegment = kRecurGradRun * kRecurGradWaves;
 

@@ -17,16 +17,12 @@
 namespace cnv {
 namespace {
 
-// state behind a piece of tokens with the given decay product and end state
-__device__ inline float through(float decay, float state, float h) { return decay < 0.0f ? state : fmaf(decay, h, state); }
-__device__ inline float joined_decay(float before, float decay) { return before < 0.0f || decay < 0.0f ? -1.0f : before * decay; }
-
 // ENDS: the first pass, which leaves only each chunk's decay and end state.
 template <class E, bool ENDS>
 __global__ __launch_bounds__(64 * kRecurWaves) void recur_kernel(RecurArgs a)
 {
     constexpr int T = kRecurRun, W = kRecurWaves;
-    __shared__ uint32_t bits[FirstTokens::kWords];
+    __shared__ uint32_t bits[RecurChunk::kWords];
     __shared__ float ends[2][2][W][64];
     using S = typename E::S;
     const int lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64);
@@ -39,86 +35,96 @@ __global__ __launch_bounds__(64 * kRecurWaves) void recur_kernel(RecurArgs a)
                 a.final_state[s * a.d + c] = a.initial ? a.initial[s * a.d + c] : 0.0f;
         return;
     }
-    const FirstTokens first(a.q, bits, a.chunk, blockIdx.x);
+    const RecurChunk chunk(a, bits, blockIdx.x);
     const RecurChannel ch(a.A, a.r_bias, a.i_bias, c);
-    const RowWalk xw(a.xs, a.q), rw(a.rs, a.q), iw(a.is, a.q), zw(a.zs, a.q);
-    const S *xp = (const S *)a.x + c, *rp = (const S *)a.r + c, *ip = (const S *)a.i + c, *zp = (const S *)a.z + c;
+    const RecurRows<E> xr(a.x, a.xs, chunk, a.q.len, a.per_seq, c), rr(a.r, a.rs, chunk, a.q.len, a.per_seq, c);
+    const RecurRows<E> ir(a.i, a.is, chunk, a.q.len, a.per_seq, c), zr(a.z, a.zs, chunk, a.q.len, a.per_seq, c);
+    const bool gate = !ENDS && a.z;
 
     float carry = 0.0f, total = 1.0f;
     if (!ENDS && a.joined)
-        for (int k = 0; k < (int)blockIdx.x; ++k)
+        for (int k = chunk.before; k < (int)blockIdx.x; ++k)
             carry = through(a.chunk_decay[(long long)k * a.d + c], a.chunk_state[(long long)k * a.d + c], carry);
 
-    const int len = (int)(first.end - first.c0);  // tokens of this chunk, none if negative
-    for (int at0 = 0, buf = 0; at0 < len; at0 += T * W, buf ^= 1) {
-        const int at = at0 + wave * T;
-        const long long t0 = first.c0 + at;
-        int n = len - at;
-        n = n < 0 ? 0 : n > T ? T : n;
-        const int skip = t0 < first.lo ? (first.lo - t0 < n ? (int)(first.lo - t0) : n) : 0;
-        const uint32_t f = n > 0 ? first.run<T>(at) : 0u;
-        const long long s0 = a.q.start || n <= 0 ? 0 : t0 / a.q.len;
+    // the next segment's values are under way while one is computed
+    S xs[T], rs[T], is[T], zs[T];
+    auto load = [&](const RecurRun<T> &run) {
+        xr.load(run, xs);
+        rr.load(run, rs);
+        ir.load(run, is);
+        if (gate) zr.load(run, zs);
+    };
+    if (chunk.len > 0) load(RecurRun<T>(chunk, wave * T));
+    for (int at0 = 0, buf = 0; at0 < chunk.len; at0 += T * W, buf ^= 1) {
+        const RecurRun<T> run(chunk, at0 + wave * T);
         float av[T], bv[T], zv[T];
-        if (n > 0) {
 #pragma unroll
-            for (int j = 0; j < T; ++j) {
-                const int k = j < n ? j : n - 1;
-                const long long s = s0 + __builtin_popcount(f & ((2u << k) - 2));
-                const float x = E::to(xp[xw.at(t0 + k, s)]), r = E::to(rp[rw.at(t0 + k, s)]), i = E::to(ip[iw.at(t0 + k, s)]);
-                zv[j] = !ENDS && a.z ? E::to(zp[zw.at(t0 + k, s)]) : 0.0f;
-                const float L = ch.A * sigmoid_f32(r + ch.rb);
-                const float dec = __builtin_amdgcn_exp2f(L * kLog2e);
-                const bool there = j < n && j >= skip;
-                av[j] = there ? dec : 1.0f;
-                bv[j] = there ? __builtin_amdgcn_sqrtf(one_minus_square(L, dec)) * sigmoid_f32(i + ch.ib) * x : 0.0f;
+        for (int j = 0; j < T; ++j) {
+            const float L = ch.A * sigmoid_f32(E::to(rs[j]) + ch.rb);
+            av[j] = __builtin_amdgcn_exp2f(L * kLog2e);
+            bv[j] = __builtin_amdgcn_sqrtf(one_minus_square(L, av[j])) * sigmoid_f32(E::to(is[j]) + ch.ib) * E::to(xs[j]);
+            if (gate) {
+                const float z = E::to(zs[j]);
+                zv[j] = z * sigmoid_f32(z);
             }
         }
+        load(RecurRun<T>(chunk, at0 + T * W + wave * T));
+        if (run.n < T)
+#pragma unroll
+            for (int j = 0; j < T; ++j) {
+                av[j] = j < run.n ? av[j] : 1.0f;
+                bv[j] = j < run.n ? bv[j] : 0.0f;
+            }
         // the state before token j where it is a sequence's first
         auto initial = [&](int j) {
-            return a.initial ? a.initial[(long long)a.q.find(t0 + j) * a.d + c] : 0.0f;
+            return a.initial ? a.initial[(long long)a.q.find(run.t0 + j) * a.d + c] : 0.0f;
         };
-        float dec = 1.0f, state = 0.0f;
-        if (n > 0) {
-            if ((f & ((1u << n) - 1)) == 0) {
+        float dec = 1.0f, end = 0.0f;
+        if (run.f == 0) {
 #pragma unroll
-                for (int j = 0; j < T; ++j) {
-                    dec *= av[j];
-                    state = fmaf(av[j], state, bv[j]);
-                }
-            } else {
+            for (int j = 0; j < T; ++j) {
+                dec *= av[j];
+                end = fmaf(av[j], end, bv[j]);
+            }
+        } else {
 #pragma unroll
-                for (int j = 0; j < T; ++j) {
-                    if (j < n && (f >> j & 1)) {
-                        dec = -1.0f;
-                        state = initial(j);
-                    }
-                    dec = dec < 0.0f ? dec : dec * av[j];
-                    state = fmaf(av[j], state, bv[j]);
+            for (int j = 0; j < T; ++j) {
+                if (run.f >> j & 1) {
+                    dec = -1.0f;
+                    end = initial(j);
                 }
+                dec = dec < 0.0f ? dec : dec * av[j];
+                end = fmaf(av[j], end, bv[j]);
             }
         }
         ends[buf][0][wave][lane] = dec;
-        ends[buf][1][wave][lane] = state;
+        ends[buf][1][wave][lane] = end;
         __syncthreads();
         float h = carry;
 #pragma unroll
         for (int w = 0; w < W; ++w) {
             const float d = ends[buf][0][w][lane], e = ends[buf][1][w][lane];
-            if (w < wave) h = through(d, e, h);
             carry = through(d, e, carry);
+            if (w < wave) h = carry;
             if (ENDS) total = joined_decay(total, d);
         }
         if (ENDS) continue;
+        S *y = (S *)a.y + run.t0 * a.d;
+        if (run.n == T && run.f == 0 && (run.last == 0 || !a.final_state)) {
 #pragma unroll
-        for (int j = 0; j < T; ++j) {
-            if (j < n) {
-                if (f >> j & 1) h = initial(j);
+            for (int j = 0; j < T; ++j) {
                 h = fmaf(av[j], h, bv[j]);
-                const float y = a.z ? h * (zv[j] * sigmoid_f32(zv[j])) : h;
-                if (mine) ((S *)a.y)[(t0 + j) * a.d + c] = E::from(y);
-                // a sequence's last token: another begins behind it, or nothing does
-                if (a.final_state && j >= skip && (f >> (j + 1) & 1 || t0 + j + 1 == first.hi)) {
-                    const int s = a.q.find(t0 + j);
+                if (mine) y[(uint32_t)(j * a.d) + (uint32_t)c] = E::from(gate ? h * zv[j] : h);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < T; ++j) {
+                if (j >= run.n) break;
+                if (run.f >> j & 1) h = initial(j);
+                h = fmaf(av[j], h, bv[j]);
+                if (mine) y[(uint32_t)(j * a.d) + (uint32_t)c] = E::from(gate ? h * zv[j] : h);
+                if (a.final_state && run.last >> j & 1) {
+                    const int s = a.q.find(run.t0 + j);
                     if (mine) a.final_state[(long long)s * a.d + c] = h;
                 }
             }

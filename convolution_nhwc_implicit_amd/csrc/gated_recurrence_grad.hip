@@ -17,35 +17,6 @@
 namespace cnv {
 namespace {
 
-__device__ inline float through(float decay, float state, float h) { return decay < 0.0f ? state : fmaf(decay, h, state); }
-__device__ inline float joined_decay(float before, float decay) { return before < 0.0f || decay < 0.0f ? -1.0f : before * decay; }
-
-// A wave's run of tokens in a segment.
-template <int T>
-struct Run {
-    long long t0, s0;
-    int n, skip;    // tokens that are there; of them, tokens before the first sequence
-    uint32_t f;     // which begin a sequence (bit T: the one behind the run)
-    uint32_t last;  // which end one
-    __device__ inline Run(const RecurArgs &a, const FirstTokens &first, int at, int len)
-    {
-        t0 = first.c0 + at;
-        n = len - at;
-        n = n < 0 ? 0 : n > T ? T : n;
-        skip = t0 < first.lo ? (first.lo - t0 < n ? (int)(first.lo - t0) : n) : 0;
-        f = n > 0 ? first.run<T>(at) : 0u;
-        last = f >> 1;
-        if (n > 0 && t0 + n == first.hi) last |= 1u << (n - 1);
-        last &= (1u << n) - 1;
-        f &= (1u << n) - 1;
-        s0 = a.q.start || n <= 0 ? 0 : t0 / a.q.len;
-    }
-    __device__ inline bool there(int j) const { return j < n && j >= skip; }
-    // the row that stands for token j, and its sequence among dense ones
-    __device__ inline long long token(int j) const { return t0 + (j < n ? j : n - 1); }
-    __device__ inline long long seq(int j) const { return s0 + __builtin_popcount(f & ((2u << (j < n ? j : n - 1)) - 2)); }
-};
-
 struct Token {
     float g, u, L, a, x;
     template <class E>
@@ -61,71 +32,147 @@ struct Token {
     }
 };
 
+// A run's values as they lie in memory.
+template <class E, int T>
+struct Loads {
+    typename E::S x[T], r[T], i[T], z[T], dy[T];
+};
+template <class E>
+struct Tensors {
+    RecurRows<E> x, r, i, z, dy;
+    bool gate;
+    __device__ inline Tensors(const RecurArgs &a, const RecurChunk &k, int c)
+        : x(a.x, a.xs, k, a.q.len, a.per_seq, c), r(a.r, a.rs, k, a.q.len, a.per_seq, c), i(a.i, a.is, k, a.q.len, a.per_seq, c),
+          z(a.z, a.zs, k, a.q.len, a.per_seq, c), dy(a.dy, a.dys, k, a.q.len, a.per_seq, c), gate(a.z != nullptr)
+    {
+    }
+    template <bool BACK, int T>
+    __device__ inline void load(const RecurRun<T> &run, Loads<E, T> &v) const
+    {
+        x.load(run, v.x);
+        r.load(run, v.r);
+        i.load(run, v.i);
+        if (BACK) {
+            dy.load(run, v.dy);
+            if (gate) z.load(run, v.z);
+        }
+    }
+};
+
+// What a run does to a state, and to the gradient that flows back through it.
+struct Piece {
+    float dec = 1.0f, end = 0.0f, bdec = 1.0f, flow = 0.0f;
+};
+template <int T>
+__device__ inline void state_piece(const RecurArgs &a, const RecurRun<T> &run, int c, const float (&av)[T], const float (&bv)[T], Piece &p)
+{
+    if (run.f == 0) {
+#pragma unroll
+        for (int j = 0; j < T; ++j) {
+            p.dec *= av[j];
+            p.end = fmaf(av[j], p.end, bv[j]);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < T; ++j) {
+            if (run.f >> j & 1) {
+                p.dec = -1.0f;
+                p.end = a.initial ? a.initial[(long long)a.q.find(run.t0 + j) * a.d + c] : 0.0f;
+            }
+            p.dec = p.dec < 0.0f ? p.dec : p.dec * av[j];
+            p.end = fmaf(av[j], p.end, bv[j]);
+        }
+    }
+}
+template <int T>
+__device__ inline float final_gradient(const RecurArgs &a, const RecurRun<T> &run, int c, int j)
+{
+    return a.dfinal ? a.dfinal[(long long)a.q.find(run.t0 + j) * a.d + c] : 0.0f;
+}
+template <int T>
+__device__ inline void flow_piece(const RecurArgs &a, const RecurRun<T> &run, int c, const float (&av)[T], const float (&G)[T], Piece &p)
+{
+    if (run.last == 0) {
+#pragma unroll
+        for (int j = T - 1; j >= 0; --j) {
+            p.flow = av[j] * (p.flow + G[j]);
+            p.bdec *= av[j];
+        }
+    } else {
+#pragma unroll
+        for (int j = T - 1; j >= 0; --j) {
+            if (run.last >> j & 1) {
+                p.bdec = -1.0f;
+                p.flow = final_gradient(a, run, c, j);
+            }
+            p.flow = av[j] * (p.flow + G[j]);
+            p.bdec = p.bdec < 0.0f ? p.bdec : p.bdec * av[j];
+        }
+    }
+}
+// tokens that are not there: nothing decays, nothing comes in
+template <int T>
+__device__ inline void cut_run(const RecurRun<T> &run, float (&av)[T], float (&in)[T])
+{
+    if (run.n < T)
+#pragma unroll
+        for (int j = 0; j < T; ++j) {
+            av[j] = j < run.n ? av[j] : 1.0f;
+            in[j] = j < run.n ? in[j] : 0.0f;
+        }
+}
+
 // The first walk.  BACK: sequences may go on in another chunk, which needs the
 // gradient's flow through this one.
 template <class E, bool BACK>
 __global__ __launch_bounds__(64 * kRecurGradWaves) void recur_states_kernel(RecurArgs a)
 {
     constexpr int T = kRecurGradRun, W = kRecurGradWaves;
-    __shared__ uint32_t bits[FirstTokens::kWords];
+    __shared__ uint32_t bits[RecurChunk::kWords];
     __shared__ float ends[2][BACK ? 4 : 2][W][64];
-    using S = typename E::S;
     const int lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64);
     const int cx = blockIdx.y * kRecurChannels + lane, c = cx < a.d ? cx : a.d - 1;
     const bool mine = cx < a.d;
-    const FirstTokens first(a.q, bits, a.chunk, blockIdx.x);
+    const RecurChunk chunk(a, bits, blockIdx.x);
     const RecurChannel ch(a.A, a.r_bias, a.i_bias, c);
-    const RowWalk xw(a.xs, a.q), rw(a.rs, a.q), iw(a.is, a.q), zw(a.zs, a.q), dyw(a.dys, a.q);
-    const S *xp = (const S *)a.x + c, *rp = (const S *)a.r + c, *ip = (const S *)a.i + c;
-    const S *zp = (const S *)a.z + c, *dyp = (const S *)a.dy + c;
+    const Tensors<E> in(a, chunk, c);
     float decay = 1.0f, state = 0.0f, bdecay = 1.0f, flow = 0.0f;
-    const int len = (int)(first.end - first.c0);
     long long seg = (long long)blockIdx.x * (a.chunk / (T * W));
-    for (int at0 = 0, buf = 0; at0 < len; at0 += T * W, buf ^= 1, ++seg) {
-        const Run<T> run(a, first, at0 + wave * T, len);
+    Loads<E, T> v;
+    if (chunk.len > 0) in.template load<BACK>(RecurRun<T>(chunk, wave * T), v);
+    for (int at0 = 0, buf = 0; at0 < chunk.len; at0 += T * W, buf ^= 1, ++seg) {
+        const RecurRun<T> run(chunk, at0 + wave * T);
         if (wave == 0 && mine) {
             a.seg_decay[seg * a.d + c] = decay;
             a.seg_state[seg * a.d + c] = state;
         }
-        float dec = 1.0f, st = 0.0f, bdec = 1.0f, fl = 0.0f;
-        if (run.n > 0) {
+        float av[T], bv[T], G[T];
 #pragma unroll
-            for (int j = 0; j < T; ++j) {
-                const long long t = run.token(j), s = run.seq(j);
-                const float x = E::to(xp[xw.at(t, s)]), r = E::to(rp[rw.at(t, s)]), i = E::to(ip[iw.at(t, s)]);
-                float G = 0.0f;
-                if (BACK) {
-                    G = E::to(dyp[dyw.at(t, s)]);
-                    if (a.z) {
-                        const float z = E::to(zp[zw.at(t, s)]);
-                        G *= z * sigmoid_f32(z);
-                    }
-                }
-                const Token k = Token::of(ch, E{}, r, i, x);
-                if (run.there(j)) {
-                    const float b = __builtin_amdgcn_sqrtf(one_minus_square(k.L, k.a)) * k.u * k.x;
-                    if (run.f >> j & 1) {
-                        dec = -1.0f;
-                        st = a.initial ? a.initial[(long long)a.q.find(run.t0 + j) * a.d + c] : 0.0f;
-                    }
-                    dec = dec < 0.0f ? dec : dec * k.a;
-                    st = fmaf(k.a, st, b);
-                    if (BACK && bdec >= 0.0f) {
-                        bdec *= k.a;
-                        fl = fmaf(bdec, G, fl);
-                        if (run.last >> j & 1) {
-                            if (a.dfinal) fl = fmaf(bdec, a.dfinal[(long long)a.q.find(run.t0 + j) * a.d + c], fl);
-                            bdec = -1.0f;
-                        }
-                    }
+        for (int j = 0; j < T; ++j) {
+            const Token k = Token::of(ch, E{}, E::to(v.r[j]), E::to(v.i[j]), E::to(v.x[j]));
+            av[j] = k.a;
+            bv[j] = __builtin_amdgcn_sqrtf(one_minus_square(k.L, k.a)) * k.u * k.x;
+            if (BACK) {
+                G[j] = E::to(v.dy[j]);
+                if (in.gate) {
+                    const float z = E::to(v.z[j]);
+                    G[j] *= z * sigmoid_f32(z);
                 }
             }
         }
-        ends[buf][0][wave][lane] = dec;
-        ends[buf][1][wave][lane] = st;
+        in.template load<BACK>(RecurRun<T>(chunk, at0 + T * W + wave * T), v);
+        cut_run(run, av, bv);
+        Piece p;
+        state_piece(a, run, c, av, bv, p);
         if constexpr (BACK) {
-            ends[buf][2][wave][lane] = bdec;
-            ends[buf][3][wave][lane] = fl;
+            cut_run(run, av, G);
+            flow_piece(a, run, c, av, G, p);
+        }
+        ends[buf][0][wave][lane] = p.dec;
+        ends[buf][1][wave][lane] = p.end;
+        if constexpr (BACK) {
+            ends[buf][2][wave][lane] = p.bdec;
+            ends[buf][3][wave][lane] = p.flow;
         }
         __syncthreads();
 #pragma unroll
@@ -152,7 +199,7 @@ template <class E>
 __global__ __launch_bounds__(64 * kRecurGradWaves) void recur_grad_kernel(RecurArgs a)
 {
     constexpr int T = kRecurGradRun, W = kRecurGradWaves;
-    __shared__ uint32_t bits[FirstTokens::kWords];
+    __shared__ uint32_t bits[RecurChunk::kWords];
     __shared__ float ends[2][4][W][64];
     using S = typename E::S;
     const int lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64);
@@ -165,68 +212,52 @@ __global__ __launch_bounds__(64 * kRecurGradWaves) void recur_grad_kernel(RecurA
                 a.dinitial[s * a.d + c] = a.dfinal ? a.dfinal[s * a.d + c] : 0.0f;
         return;
     }
-    const FirstTokens first(a.q, bits, a.chunk, blockIdx.x);
+    const RecurChunk chunk(a, bits, blockIdx.x);
     const RecurChannel ch(a.A, a.r_bias, a.i_bias, c);
-    const RowWalk xw(a.xs, a.q), rw(a.rs, a.q), iw(a.is, a.q), zw(a.zs, a.q), dyw(a.dys, a.q);
-    const S *xp = (const S *)a.x + c, *rp = (const S *)a.r + c, *ip = (const S *)a.i + c;
-    const S *zp = (const S *)a.z + c, *dyp = (const S *)a.dy + c;
+    const Tensors<E> in(a, chunk, c);
     float before = 0.0f, flow = 0.0f;  // the state the chunk starts with; the gradient that flows in behind it
     if (a.joined) {
-        for (int k = 0; k < (int)blockIdx.x; ++k)
+        const int after = a.per_seq ? chunk.before + a.per_seq : a.chunks;
+        for (int k = chunk.before; k < (int)blockIdx.x; ++k)
             before = through(a.chunk_decay[(long long)k * a.d + c], a.chunk_state[(long long)k * a.d + c], before);
-        for (int k = a.chunks - 1; k > (int)blockIdx.x; --k)
+        for (int k = after - 1; k > (int)blockIdx.x; --k)
             flow = through(a.back_decay[(long long)k * a.d + c], a.chunk_back[(long long)k * a.d + c], flow);
     }
     float dll = 0.0f, drb = 0.0f, dib = 0.0f;
-    const int len = (int)(first.end - first.c0), segs = len > 0 ? (len + T * W - 1) / (T * W) : 0;
+    const int segs = (chunk.len + T * W - 1) / (T * W);
+    Loads<E, T> v;
+    if (segs > 0) in.template load<true>(RecurRun<T>(chunk, ((segs - 1) * W + wave) * T), v);
     for (int sg = segs - 1, buf = 0; sg >= 0; --sg, buf ^= 1) {
-        const Run<T> run(a, first, (sg * W + wave) * T, len);
-        float xv[T], gv[T], uv[T], Lv[T], av[T], wv[T], zv[T], dv[T];
-        float dec = 1.0f, st = 0.0f, bdec = 1.0f, fl = 0.0f;
-        auto initial = [&](int j) {
-            return a.initial ? a.initial[(long long)a.q.find(run.t0 + j) * a.d + c] : 0.0f;
-        };
-        auto dfinal = [&](int j) {
-            return a.dfinal ? a.dfinal[(long long)a.q.find(run.t0 + j) * a.d + c] : 0.0f;
-        };
-        if (run.n > 0) {
+        const RecurRun<T> run(chunk, (sg * W + wave) * T);
+        float xv[T], gv[T], uv[T], Lv[T], av[T], bv[T], wv[T], zv[T], dv[T], G[T];
 #pragma unroll
-            for (int j = 0; j < T; ++j) {
-                const long long t = run.token(j), s = run.seq(j);
-                const float x = E::to(xp[xw.at(t, s)]), r = E::to(rp[rw.at(t, s)]), i = E::to(ip[iw.at(t, s)]);
-                dv[j] = E::to(dyp[dyw.at(t, s)]);
-                zv[j] = a.z ? E::to(zp[zw.at(t, s)]) : 0.0f;
-                const Token k = Token::of(ch, E{}, r, i, x);
-                const bool there = run.there(j);
-                xv[j] = there ? x : 0.0f;
-                gv[j] = k.g;
-                uv[j] = k.u;
-                Lv[j] = k.L;
-                av[j] = there ? k.a : 1.0f;
-                wv[j] = there ? one_minus_square(k.L, k.a) : 0.0f;
-                const float b = __builtin_amdgcn_sqrtf(wv[j]) * k.u * xv[j];
-                if (there) {
-                    if (run.f >> j & 1) {
-                        dec = -1.0f;
-                        st = initial(j);
-                    }
-                    dec = dec < 0.0f ? dec : dec * k.a;
-                    st = fmaf(k.a, st, b);
-                    if (bdec >= 0.0f) {
-                        bdec *= k.a;
-                        fl = fmaf(bdec, a.z ? dv[j] * (zv[j] * sigmoid_f32(zv[j])) : dv[j], fl);
-                        if (run.last >> j & 1) {
-                            fl = fmaf(bdec, dfinal(j), fl);
-                            bdec = -1.0f;
-                        }
-                    }
-                }
+        for (int j = 0; j < T; ++j) {
+            const Token k = Token::of(ch, E{}, E::to(v.r[j]), E::to(v.i[j]), E::to(v.x[j]));
+            xv[j] = k.x;
+            gv[j] = k.g;
+            uv[j] = k.u;
+            Lv[j] = k.L;
+            av[j] = k.a;
+            wv[j] = one_minus_square(k.L, k.a);
+            bv[j] = __builtin_amdgcn_sqrtf(wv[j]) * k.u * k.x;
+            dv[j] = E::to(v.dy[j]);
+            zv[j] = 0.0f;
+            G[j] = dv[j];
+            if (in.gate) {
+                zv[j] = E::to(v.z[j]);
+                G[j] *= zv[j] * sigmoid_f32(zv[j]);
             }
         }
-        ends[buf][0][wave][lane] = dec;
-        ends[buf][1][wave][lane] = st;
-        ends[buf][2][wave][lane] = bdec;
-        ends[buf][3][wave][lane] = fl;
+        if (sg > 0) in.template load<true>(RecurRun<T>(chunk, ((sg - 1) * W + wave) * T), v);
+        cut_run(run, av, bv);
+        cut_run(run, av, G);
+        Piece p;
+        state_piece(a, run, c, av, bv, p);
+        flow_piece(a, run, c, av, G, p);
+        ends[buf][0][wave][lane] = p.dec;
+        ends[buf][1][wave][lane] = p.end;
+        ends[buf][2][wave][lane] = p.bdec;
+        ends[buf][3][wave][lane] = p.flow;
         __syncthreads();
         const long long seg = (long long)blockIdx.x * (a.chunk / (T * W)) + sg;
         float h = through(a.seg_decay[seg * a.d + c], a.seg_state[seg * a.d + c], before);
@@ -236,32 +267,30 @@ __global__ __launch_bounds__(64 * kRecurGradWaves) void recur_grad_kernel(RecurA
             if (w < wave) h = through(ends[buf][0][w][lane], ends[buf][1][w][lane], h);
 #pragma unroll
         for (int w = W - 1; w >= 0; --w) {
-            const float d = ends[buf][2][w][lane], e = ends[buf][3][w][lane];
-            if (w > wave) k = through(d, e, k);
-            flow = through(d, e, flow);
+            flow = through(ends[buf][2][w][lane], ends[buf][3][w][lane], flow);
+            if (w > wave) k = flow;
         }
         float hv[T];  // the states before each token
 #pragma unroll
         for (int j = 0; j < T; ++j) {
-            if (run.there(j) && (run.f >> j & 1)) h = initial(j);
+            if (run.f >> j & 1) h = a.initial ? a.initial[(long long)a.q.find(run.t0 + j) * a.d + c] : 0.0f;
             hv[j] = h;
-            if (run.there(j)) h = fmaf(av[j], h, __builtin_amdgcn_sqrtf(wv[j]) * uv[j] * xv[j]);
+            h = fmaf(av[j], h, bv[j]);
         }
 #pragma unroll
         for (int j = T - 1; j >= 0; --j) {
-            if (!run.there(j)) continue;
-            if (run.last >> j & 1) k = dfinal(j);
+            if (j >= run.n) continue;
+            if (run.last >> j & 1) k = final_gradient(a, run, c, j);
             const float root = __builtin_amdgcn_rsqf(fmaxf(wv[j], 1.2e-38f)), size = wv[j] * root;
-            const float in = uv[j] * xv[j], b = size * in, hj = fmaf(av[j], hv[j], b);
-            float G = dv[j], dz = 0.0f;
-            if (a.z) {
+            const float in_ = uv[j] * xv[j], hj = fmaf(av[j], hv[j], bv[j]);
+            float dz = 0.0f;
+            if (in.gate) {
                 const float s = sigmoid_f32(zv[j]);
-                G *= zv[j] * s;
                 dz = dv[j] * hj * (s * (1.0f + zv[j] * (1.0f - s)));
             }
-            k += G;
-            const float dl = k * (av[j] * hv[j] * Lv[j] - av[j] * av[j] * in * (Lv[j] * root));  // dL * L
-            const float dr = dl * (1.0f - gv[j]), di = k * b * (1.0f - uv[j]);
+            k += G[j];
+            const float dl = k * (av[j] * hv[j] * Lv[j] - av[j] * av[j] * in_ * (Lv[j] * root));  // dL * L
+            const float dr = dl * (1.0f - gv[j]), di = k * bv[j] * (1.0f - uv[j]);
             dll += dl;
             drb += dr;
             dib += di;
@@ -270,7 +299,7 @@ __global__ __launch_bounds__(64 * kRecurGradWaves) void recur_grad_kernel(RecurA
                 ((S *)a.dx)[at] = E::from(k * size * uv[j]);
                 ((S *)a.dr)[at] = E::from(dr);
                 ((S *)a.di)[at] = E::from(di);
-                if (a.z) ((S *)a.dz)[at] = E::from(dz);
+                if (in.gate) ((S *)a.dz)[at] = E::from(dz);
             }
             k *= av[j];
             if ((run.f >> j & 1) && a.dinitial && mine) a.dinitial[(long long)a.q.find(run.t0 + j) * a.d + c] = k;
