@@ -22,33 +22,48 @@ int check_recurrence(const gated_recurrence_problem_t *p, int dtype, bool grad)
         if (r == CONV2D_OK) r = check_stride(*s);
     if (r == CONV2D_OK && grad) r = check_stride(p->dy);
     if (r != CONV2D_OK) return r;
-    if (!float_type(dtype) || p->d > kMaxStride || ceil_div(p->d, kRecurChannels) > kMaxGridY) return CONV2D_ERR_UNSUPPORTED;
+    if (!float_type(dtype) || p->d > kMaxStride) return CONV2D_ERR_UNSUPPORTED;
     return CONV2D_OK;
 }
 
 struct RecurPlan {
-    int chunk, chunks, joined, per_seq;
+    RecurShape shape;
+    int across, chunk, chunks, joined, per_seq;
     size_t per_chunk, per_segment;  // bytes of a value for each of them and channel
 };
 
 // Whether one stride reaches all rows of a batch.
 bool one_stride(const seq_batch_t &b, const seq_stride_t &s) { return b.seq_start || b.seqs == 1 || s.seq == b.len * s.row; }
 
-// Tokens of a chunk: sequences stay whole where that alone fills the chip (a workgroup
-// to a compute unit), since cut ones are read twice; else about two workgroups to each.
+// Sequences are walked whole where that alone gives every compute unit a workgroup, for
+// chunks are read twice; else they are cut so that each unit has as many workgroups as
+// it holds: two in the forward pass, one in the gradient's.  (8192 tokens of 4096 bf16
+// channels: forward 132 us with two, 139 with one; 3 x 517 of 768, gradients: 48 us with
+// one, 58 with two.)  A row's 128 bytes to a workgroup: with 64 of them and twice the
+// workgroups the walks take 150 us, and the training step 730 instead of 530.
 // Chunks run over all tokens, sequences' borders inside them, unless a dense batch's
 // sequences lie apart.
-RecurPlan recur_plan(const gated_recurrence_problem_t *p, int segment, bool grad)
+RecurPlan recur_plan(const gated_recurrence_problem_t *p, int dtype, bool grad)
 {
     const seq_batch_t &b = p->batch;
     bool flat = one_stride(b, p->x) && one_stride(b, p->r) && one_stride(b, p->i) && one_stride(b, p->z);
     if (grad) flat = flat && one_stride(b, p->dy);
-    const long long across = ceil_div(p->d, kRecurChannels), pieces = ceil_div(2 * kCUs, across);
-    const long long most = flat ? b.tokens : b.len;  // tokens that a chunk can have
-    long long chunk = ceil_div(ceil_div(b.tokens, pieces), segment) * segment;
-    if (!b.seq_start && b.len > 0 && b.len % segment == 0 && across * b.seqs >= kCUs) chunk = b.len;
-    chunk = std::min(std::min<long long>(std::max<long long>(chunk, segment), kRecurChunkMost), std::max(1LL, ceil_div(most, segment)) * segment);
     RecurPlan r;
+    r.shape = {32, dtype != CONV2D_DTYPE_F32 ? 2 : 1};
+    if (p->d < r.shape.vc) r.shape = {8, 1};
+    // sequences that are walked whole; all tokens together where their lengths are on the device
+    const long long walks = b.seq_start ? 1 : b.seqs;
+    while (r.shape.lanes > 8 && p->d <= r.shape.channels() / 2) r.shape.lanes /= 2;
+    const int segment = recur_segment(r.shape);
+    const long long across = ceil_div(p->d, r.shape.channels());
+    long long chunk = b.tokens;
+    if (across * walks < kCUs) chunk = ceil_div(b.tokens, ceil_div(grad ? kCUs : 2 * kCUs, across));
+    else if (!b.seq_start && b.len >= segment) {
+        chunk = b.len;
+        if (b.len % segment) flat = false;
+    }
+    chunk = std::min(std::max(1LL, ceil_div(std::min(chunk, flat ? b.tokens : b.len), segment)) * segment, (long long)kRecurChunkMost);
+    r.across = (int)across;
     r.chunk = (int)chunk;
     r.per_seq = flat ? 0 : (int)ceil_div(b.len, chunk);
     r.chunks = flat ? (int)ceil_div(b.tokens, chunk) : r.per_seq * b.seqs;
@@ -62,10 +77,9 @@ size_t recur_grad_bytes(const gated_recurrence_problem_t *p, const RecurPlan &r)
 {
     return up((size_t)r.chunks * 3 * p->d * 4) + 2 * r.per_segment + (r.joined ? 4 * r.per_chunk : 0);
 }
-// launches: 512 threads a chunk, and for 256 sequences
 bool recur_fits(const gated_recurrence_problem_t *p, const RecurPlan &r)
 {
-    return fits((long long)r.chunks + ceil_div(p->batch.seqs, kRecurStateSeqs), 64 * 16);
+    return fits((r.chunks + ceil_div(p->batch.seqs, kRecurStateSeqs)) * r.across + 8, 64 * kRecurWaves);
 }
 
 RecurArgs recur_args(const gated_recurrence_problem_t *p, const RecurPlan &r)
@@ -75,6 +89,8 @@ RecurArgs recur_args(const gated_recurrence_problem_t *p, const RecurPlan &r)
     a.d = p->d;
     a.chunk = r.chunk;
     a.chunks = r.chunks;
+    a.across = r.across;
+    a.tail = r.per_seq ? p->batch.seqs : 1;
     a.joined = r.joined;
     a.per_seq = r.per_seq;
     a.xs = stride_of(p->x);
@@ -144,7 +160,7 @@ int gated_recurrence_workspace_size(const gated_recurrence_problem_t *prob, int 
     const int r = check_recurrence(prob, dtype, false);
     if (r != CONV2D_OK) return r;
     if (!bytes) return CONV2D_ERR_INVALID_ARGUMENT;
-    const RecurPlan plan = recur_plan(prob, kRecurSegment, false);
+    const RecurPlan plan = recur_plan(prob, dtype, false);
     if (!recur_fits(prob, plan)) return CONV2D_ERR_UNSUPPORTED;
     *bytes = recur_bytes(plan);
     return CONV2D_OK;
@@ -161,7 +177,7 @@ int gated_recurrence(const gated_recurrence_problem_t *prob, int dtype, const vo
     if (!all_aligned(bytes_of(dtype), {x, r, i, z, y}) || !all_aligned(4, {A, r_bias, i_bias, initial_state, final_state}) ||
         !aligned(workspace, 16))
         return CONV2D_ERR_UNSUPPORTED;
-    const RecurPlan plan = recur_plan(prob, kRecurSegment, false);
+    const RecurPlan plan = recur_plan(prob, dtype, false);
     if (!recur_fits(prob, plan)) return CONV2D_ERR_UNSUPPORTED;
     const size_t need = recur_bytes(plan);
     if (need && !workspace) return CONV2D_ERR_INVALID_ARGUMENT;
@@ -183,7 +199,7 @@ int gated_recurrence(const gated_recurrence_problem_t *prob, int dtype, const vo
         a.chunk_decay = w.take(plan.per_chunk);
         a.chunk_state = w.take(plan.per_chunk);
     }
-    return status(launch_recurrence(dtype, a, (hipStream_t)stream));
+    return status(launch_recurrence(dtype, a, plan.shape, (hipStream_t)stream));
 }
 
 int gated_recurrence_grad_workspace_size(const gated_recurrence_problem_t *prob, int dtype, size_t *bytes)
@@ -191,7 +207,7 @@ int gated_recurrence_grad_workspace_size(const gated_recurrence_problem_t *prob,
     const int r = check_recurrence(prob, dtype, true);
     if (r != CONV2D_OK) return r;
     if (!bytes) return CONV2D_ERR_INVALID_ARGUMENT;
-    const RecurPlan plan = recur_plan(prob, kRecurGradSegment, true);
+    const RecurPlan plan = recur_plan(prob, dtype, true);
     if (!recur_fits(prob, plan)) return CONV2D_ERR_UNSUPPORTED;
     *bytes = recur_grad_bytes(prob, plan);
     return CONV2D_OK;
@@ -211,7 +227,7 @@ int gated_recurrence_grad(const gated_recurrence_problem_t *prob, int dtype, con
         !all_aligned(4, {A, r_bias, i_bias, initial_state, dfinal, g->dA, g->dr_bias, g->di_bias, g->dinitial}) ||
         !aligned(workspace, 16))
         return CONV2D_ERR_UNSUPPORTED;
-    const RecurPlan plan = recur_plan(prob, kRecurGradSegment, true);
+    const RecurPlan plan = recur_plan(prob, dtype, true);
     if (!recur_fits(prob, plan)) return CONV2D_ERR_UNSUPPORTED;
     const size_t need = recur_grad_bytes(prob, plan);
     if (need && !workspace) return CONV2D_ERR_INVALID_ARGUMENT;
@@ -242,7 +258,7 @@ int gated_recurrence_grad(const gated_recurrence_problem_t *prob, int dtype, con
         a.back_decay = w.take(plan.per_chunk);
         a.chunk_back = w.take(plan.per_chunk);
     }
-    if (hipError_t h = launch_recurrence_grad(dtype, a, (hipStream_t)stream)) return status(h);
+    if (hipError_t h = launch_recurrence_grad(dtype, a, plan.shape, (hipStream_t)stream)) return status(h);
     const ColumnSumArgs s = {a.partial, plan.chunks, 3, prob->d, {g->dA, g->dr_bias, g->di_bias}, A};
     return status(launch_column_sums(CONV2D_DTYPE_F32, s, (hipStream_t)stream));
 }
@@ -259,7 +275,7 @@ int gated_recurrence_step(const gated_recurrence_step_problem_t *p, int dtype, c
     if (!x || !r || !i || !A || !y || (p->pool > 0 && !state)) return CONV2D_ERR_INVALID_ARGUMENT;
     if (!all_aligned(bytes_of(dtype), {x, r, i, z, y}) || !all_aligned(4, {A, r_bias, i_bias, state, slots}))
         return CONV2D_ERR_UNSUPPORTED;
-    if (ceil_div(p->d, 256) > kMaxGridY || !fits(p->rows, 256)) return CONV2D_ERR_UNSUPPORTED;
+    if (ceil_div(p->d, 256 * kRecurStepChannels) > kMaxGridY || !fits(p->rows, 256)) return CONV2D_ERR_UNSUPPORTED;
     const RecurStepArgs a = {p->rows, p->pool, p->d, p->x_row, p->r_row, p->i_row, p->z_row, x, r, i, z, A, r_bias, i_bias,
                              state, slots, y};
     return status(launch_recurrence_step(dtype, a, (hipStream_t)stream));

@@ -49,14 +49,21 @@ hipError_t launch_layer_norm(int dtype, const NormArgs &a, const NormShape &s, h
 hipError_t launch_layer_norm_grad(int dtype, const NormArgs &a, const NormShape &s, hipStream_t st);
 
 // ---- gated recurrence (gated_recurrence.hip, gated_recurrence_grad.hip) -------------
-constexpr int kRecurChannels = 64;     // channels of a workgroup
+// How a workgroup's lanes lie: `lanes` of a wave along channels, `vc` channels to each;
+// a wave's other lanes, and the waves, take successive runs of tokens.
+struct RecurShape {
+    int lanes, vc;
+    constexpr int channels() const { return lanes * vc; }
+};
 constexpr int kRecurChunkMost = 1 << 15;  // tokens of a chunk: their first-token bits lie in LDS
 constexpr int kRecurStateSeqs = 256;   // sequences of a workgroup that writes the states of empty ones
 
 struct RecurArgs {
     Seqs q;
     int d;
+    int across;          // workgroups along channels
     int chunk, chunks;   // tokens of a chunk (whole segments), chunks in all
+    int tail;            // chunks that no other follows
     int joined;          // chunks start inside sequences
     int per_seq;         // chunks of each sequence; 0: chunks run over all tokens
     RowStride xs, rs, is, zs, dys;
@@ -80,12 +87,12 @@ struct RecurStepArgs {
     const int *slots;
     void *y;
 };
-constexpr int kRecurRun = 8, kRecurWaves = 8;          // forward: tokens of a wave's run, waves of a workgroup
-constexpr int kRecurGradRun = 8, kRecurGradWaves = 8;   // gradient
-constexpr int kRecurSegment = kRecurRun * kRecurWaves, kRecurGradSegment = kRecurGradRun * kRecurGradWaves;
+constexpr int kRecurRun = 4, kRecurWaves = 8;  // tokens of a lane's run, waves of a workgroup
+constexpr int kRecurStepChannels = 4;  // channels of a thread of the single-token kernel
+constexpr int recur_segment(const RecurShape &s) { return 64 / s.lanes * kRecurRun * kRecurWaves; }
 
-hipError_t launch_recurrence(int dtype, const RecurArgs &a, hipStream_t st);
-hipError_t launch_recurrence_grad(int dtype, const RecurArgs &a, hipStream_t st);
+hipError_t launch_recurrence(int dtype, const RecurArgs &a, const RecurShape &s, hipStream_t st);
+hipError_t launch_recurrence_grad(int dtype, const RecurArgs &a, const RecurShape &s, hipStream_t st);
 hipError_t launch_recurrence_step(int dtype, const RecurStepArgs &a, hipStream_t st);
 
 // ---- 4-bit products (fp4.hip) ----------------------------------------------------

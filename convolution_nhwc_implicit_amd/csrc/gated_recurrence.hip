@@ -1,13 +1,13 @@
 // gated_recurrence.hip -- gated linear recurrence: forward pass and single tokens.
 //
-//   g = sigmoid(r + r_bias), u = sigmoid(i + i_bias), a = exp(A g)
+//   g = sigmoid(r + r_bias), u = sigmoid(i + i_bias), a = exp(A g) = 2^L
 //   h = a h + sqrt(1 - a^2) u x;  y = h silu(z)
 //
-// Lanes lie along channels.  A workgroup walks 64 channels of a chunk of tokens in
-// segments; its waves take successive runs of a segment's tokens.  Each computes its
-// run's decays and inputs, the product of the decays and the state it would end with
-// from zero; these meet in LDS, every wave composes the state that its run starts with,
-// and walks the run again in registers.  Where a sequence begins inside a run, product
+// A workgroup walks some channels of a chunk of tokens in segments; groups of its lanes
+// take successive runs of a segment's tokens.  Each computes its run's decays and
+// inputs, the product of the decays and the state it would end with from zero; these
+// are joined by shuffles and through LDS, so that every lane has the state that its run
+// starts with, and walks the run again in registers.  Where a sequence begins inside a run, product
 // and state are cut off there (product -1), so that nothing of one sequence, infinities
 // and NaN among it, reaches another: runs, segments and chunks need not know sequences.
 // Chunks that begin inside a sequence get their state from a first pass over the chunks
@@ -18,186 +18,230 @@ namespace cnv {
 namespace {
 
 // ENDS: the first pass, which leaves only each chunk's decay and end state.
-template <class E, bool ENDS>
-__global__ __launch_bounds__(64 * kRecurWaves) void recur_kernel(RecurArgs a)
+// GATE: y is h silu(z).
+template <class E, int VC, int LC, bool ENDS, bool GATE>
+__global__ __launch_bounds__(64 * kRecurWaves, 4) void recur_kernel(RecurArgs a)
 {
     constexpr int T = kRecurRun, W = kRecurWaves;
+    typedef RecurPlace<VC, LC, T> Place;
+    constexpr int kSegment = W * Place::kSpan;
     __shared__ uint32_t bits[RecurChunk::kWords];
-    __shared__ float ends[2][2][W][64];
-    using S = typename E::S;
-    const int lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64);
-    const int cx = blockIdx.y * kRecurChannels + lane, c = cx < a.d ? cx : a.d - 1;
-    const bool mine = cx < a.d;
-    if (!ENDS && (int)blockIdx.x >= a.chunks) {  // final states of empty sequences
-        const long long s0 = (long long)(blockIdx.x - a.chunks) * kRecurStateSeqs;
-        for (long long s = s0 + wave; s < s0 + kRecurStateSeqs && s < a.q.seqs; s += W)
-            if (mine && a.q.begin((int)s) == a.q.end((int)s))
-                a.final_state[s * a.d + c] = a.initial ? a.initial[s * a.d + c] : 0.0f;
+    __shared__ float2 ends[2][W][LC * VC];
+    typedef RecurRaw<E, VC> Raw;
+    const int blocks = (a.chunks - (ENDS ? a.tail : 0)) * a.across, id = recur_block(blockIdx.x, blocks);
+    if ((int)blockIdx.x >= (blocks + 7) / 8 * 8) {  // final states of empty sequences
+        const int b = blockIdx.x - (blocks + 7) / 8 * 8;
+        const Place at(b % a.across, a.d);
+        const long long s0 = (long long)(b / a.across) * kRecurStateSeqs;
+        for (long long s = s0 + at.wave; s < s0 + kRecurStateSeqs && s < a.q.seqs; s += W)
+            if (at.mine && at.q == 0 && a.q.begin((int)s) == a.q.end((int)s)) {
+                float h[VC] = {};
+                if (a.initial) recur_get<VC>(a.initial, s, a.d, at.c, h);
+                recur_put<VC>(a.final_state, s, a.d, at.c, h);
+            }
         return;
     }
-    const RecurChunk chunk(a, bits, blockIdx.x);
-    const RecurChannel ch(a.A, a.r_bias, a.i_bias, c);
-    const RecurRows<E> xr(a.x, a.xs, chunk, a.q.len, a.per_seq, c), rr(a.r, a.rs, chunk, a.q.len, a.per_seq, c);
-    const RecurRows<E> ir(a.i, a.is, chunk, a.q.len, a.per_seq, c), zr(a.z, a.zs, chunk, a.q.len, a.per_seq, c);
-    const bool gate = !ENDS && a.z;
+    if (id >= blocks) return;
+    // the first pass leaves out the last chunk (of each sequence): nothing follows it
+    int index = id / a.across;
+    if (ENDS && a.per_seq) index += index / (a.per_seq - 1);
+    const Place at(id % a.across, a.d);
+    RecurChunk chunk(a, bits, index);
+    const RecurChannels<VC> ch(a.A, a.r_bias, a.i_bias, at.c);
+    const RecurRows<E, VC> xr(a.x, a.xs, a, chunk, at), rr(a.r, a.rs, a, chunk, at), ir(a.i, a.is, a, chunk, at), zr(a.z, a.zs, a, chunk, at);
+    const RecurOut<E, VC> yr(a.y, a, chunk, at);
 
-    float carry = 0.0f, total = 1.0f;
-    if (!ENDS && a.joined)
-        for (int k = chunk.before; k < (int)blockIdx.x; ++k)
-            carry = through(a.chunk_decay[(long long)k * a.d + c], a.chunk_state[(long long)k * a.d + c], carry);
-
-    // the next segment's values are under way while one is computed
-    S xs[T], rs[T], is[T], zs[T];
-    auto load = [&](const RecurRun<T> &run) {
-        xr.load(run, xs);
-        rr.load(run, rs);
-        ir.load(run, is);
-        if (gate) zr.load(run, zs);
+    // the next segment's values are under way while one is computed: a token's are asked
+    // for as soon as its registers are free
+    Raw xs[T], rs[T], is[T], zs[T];
+    struct {
+        __amdgpu_buffer_rsrc_t x, r, i, z;
+    } next;
+    auto aim = [&](const RecurSpan &span) {
+        next.x = xr.span(span);
+        next.r = rr.span(span);
+        next.i = ir.span(span);
+        if (GATE) next.z = zr.span(span);
     };
-    if (chunk.len > 0) load(RecurRun<T>(chunk, wave * T));
-    for (int at0 = 0, buf = 0; at0 < chunk.len; at0 += T * W, buf ^= 1) {
-        const RecurRun<T> run(chunk, at0 + wave * T);
-        float av[T], bv[T], zv[T];
+    auto load = [&](int j, auto inside) {
+        constexpr bool INSIDE = decltype(inside)::value;
+        rr.template load<INSIDE>(next.r, j, rs[j]);
+        ir.template load<INSIDE>(next.i, j, is[j]);
+        xr.template load<INSIDE>(next.x, j, xs[j]);
+        if (GATE) zr.template load<INSIDE>(next.z, j, zs[j]);
+    };
+    const int lead = at.wave * Place::kSpan;
+    aim(RecurSpan(chunk, at, lead));
+#pragma unroll
+    for (int j = 0; j < T; ++j) load(j, std::false_type{});
+
+    chunk.mark(a);
+    float carry[VC] = {};
+    RecurPiece<VC> total;
+    total.clear();
+    if (!ENDS && a.joined)
+#pragma unroll 4
+        for (int k = chunk.before; k < index; ++k) {
+            RecurPiece<VC> p;
+            recur_get<VC>(a.chunk_decay, k, a.d, at.c, p.dec);
+            recur_get<VC>(a.chunk_state, k, a.d, at.c, p.end);
+            p.template carry<false>(carry);
+        }
+
+    // INSIDE: this segment lies inside a sequence, and all of the next one's tokens are there
+    auto segment = [&](int seg, auto inside) {
+        constexpr bool INSIDE = decltype(inside)::value;
+        const RecurSpan span(chunk, at, seg + lead);
+        const RecurRun<T> run = INSIDE ? RecurRun<T>() : RecurRun<T>(chunk, at, span);
+        aim(RecurSpan(chunk, at, seg + lead + kSegment));
+        float av[T][VC], bv[T][VC], zv[T][VC];
 #pragma unroll
         for (int j = 0; j < T; ++j) {
-            const float L = ch.A * sigmoid_f32(E::to(rs[j]) + ch.rb);
-            av[j] = __builtin_amdgcn_exp2f(L * kLog2e);
-            bv[j] = __builtin_amdgcn_sqrtf(one_minus_square(L, av[j])) * sigmoid_f32(E::to(is[j]) + ch.ib) * E::to(xs[j]);
-            if (gate) {
-                const float z = E::to(zs[j]);
-                zv[j] = z * sigmoid_f32(z);
-            }
-        }
-        load(RecurRun<T>(chunk, at0 + T * W + wave * T));
-        if (run.n < T)
 #pragma unroll
-            for (int j = 0; j < T; ++j) {
-                av[j] = j < run.n ? av[j] : 1.0f;
-                bv[j] = j < run.n ? bv[j] : 0.0f;
-            }
-        // the state before token j where it is a sequence's first
-        auto initial = [&](int j) {
-            return a.initial ? a.initial[(long long)a.q.find(run.t0 + j) * a.d + c] : 0.0f;
-        };
-        float dec = 1.0f, end = 0.0f;
-        if (run.f == 0) {
-#pragma unroll
-            for (int j = 0; j < T; ++j) {
-                dec *= av[j];
-                end = fmaf(av[j], end, bv[j]);
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < T; ++j) {
-                if (run.f >> j & 1) {
-                    dec = -1.0f;
-                    end = initial(j);
+            for (int v = 0; v < VC; ++v) {
+                const float L = ch.A[v] * recur_gate(rs[j][v], ch.rb[v]);
+                av[j][v] = __builtin_amdgcn_exp2f(L);
+                bv[j][v] = __builtin_amdgcn_sqrtf(one_minus_square(L, av[j][v])) * recur_gate(is[j][v], ch.ib[v]) * xs[j][v];
+                if (GATE) {
+                    const float z = zs[j][v];
+                    zv[j][v] = z * sigmoid_f32(z);
                 }
-                dec = dec < 0.0f ? dec : dec * av[j];
-                end = fmaf(av[j], end, bv[j]);
             }
+            load(j, inside);
         }
-        ends[buf][0][wave][lane] = dec;
-        ends[buf][1][wave][lane] = end;
+        const long long t0 = chunk.c0 + seg + lead + at.q * T;
+        if (!INSIDE) {
+            recur_cut<VC, T>(run, bv);
+            if (run.firsts && a.initial)  // what the initial states bring is an input of the first tokens
+                recur_gather<VC, T>(a, a.initial, run.f, t0, at.c, [&](int j, const float (&h)[VC]) {
+#pragma unroll
+                    for (int v = 0; v < VC; ++v) bv[j][v] = fmaf(av[j][v], h[v], bv[j][v]);
+                });
+        }
+        RecurPiece<VC> p;
+        recur_piece<VC, T>(run.f, run.firsts, av, bv, p);
+        float h[VC];
+        const int buf = seg / kSegment & 1;
+        RecurJoin<VC, LC, W, false, INSIDE> join(p, at);
+        join.put(ends[buf]);
         __syncthreads();
-        float h = carry;
+        join.get(ends[buf], carry, h, ENDS ? &total : nullptr);
+        if (ENDS) return;
+        const __amdgpu_buffer_rsrc_t y = yr.span(span);
 #pragma unroll
-        for (int w = 0; w < W; ++w) {
-            const float d = ends[buf][0][w][lane], e = ends[buf][1][w][lane];
-            carry = through(d, e, carry);
-            if (w < wave) h = carry;
-            if (ENDS) total = joined_decay(total, d);
-        }
-        if (ENDS) continue;
-        S *y = (S *)a.y + run.t0 * a.d;
-        if (run.n == T && run.f == 0 && (run.last == 0 || !a.final_state)) {
+        for (int j = 0; j < T; ++j) {
+            float out[VC];
 #pragma unroll
-            for (int j = 0; j < T; ++j) {
-                h = fmaf(av[j], h, bv[j]);
-                if (mine) y[(uint32_t)(j * a.d) + (uint32_t)c] = E::from(gate ? h * zv[j] : h);
+            for (int v = 0; v < VC; ++v) {
+                if (!INSIDE) h[v] = run.f >> j & 1 ? 0.0f : h[v];
+                h[v] = fmaf(av[j][v], h[v], bv[j][v]);
+                out[v] = GATE ? h[v] * zv[j][v] : h[v];
+                if (!INSIDE) av[j][v] = h[v];
             }
-        } else {
-#pragma unroll
-            for (int j = 0; j < T; ++j) {
-                if (j >= run.n) break;
-                if (run.f >> j & 1) h = initial(j);
-                h = fmaf(av[j], h, bv[j]);
-                if (mine) y[(uint32_t)(j * a.d) + (uint32_t)c] = E::from(gate ? h * zv[j] : h);
-                if (a.final_state && run.last >> j & 1) {
-                    const int s = a.q.find(run.t0 + j);
-                    if (mine) a.final_state[(long long)s * a.d + c] = h;
-                }
-            }
+            yr.template store<INSIDE>(y, j, out);
         }
+        if (!INSIDE && run.lasts && a.final_state) recur_scatter<VC, T>(a, run.last, t0, at, av, a.final_state);
+    };
+    for (int seg = 0, begin = 0; seg < chunk.len; seg += kSegment) {
+        while (begin < seg) begin = chunk.next(seg, a.chunk);
+        if (begin > seg + kSegment && seg + 2 * kSegment <= chunk.len) segment(seg, std::true_type{});
+        else segment(seg, std::false_type{});
     }
-    if (ENDS && wave == 0 && mine) {
-        a.chunk_decay[(long long)blockIdx.x * a.d + c] = total;
-        a.chunk_state[(long long)blockIdx.x * a.d + c] = carry;
+    if (ENDS && at.wave == 0 && at.q == 0 && at.mine) {
+        recur_put<VC>(a.chunk_decay, index, a.d, at.c, total.dec);
+        recur_put<VC>(a.chunk_state, index, a.d, at.c, carry);
     }
 }
 
-// One token: a thread to a channel of a row.
-template <class E>
+// One token: a thread to VC channels of a row.  The last one's loads are moved back as
+// above; states are updated in place, so it writes only the channels that are its own.
+template <class E, int VC>
 __global__ __launch_bounds__(256) void recur_step_kernel(RecurStepArgs a)
 {
     using S = typename E::S;
-    const int c = blockIdx.y * 256 + threadIdx.x;
-    if (c >= a.d) return;
+    const int cx = (blockIdx.y * 256 + threadIdx.x) * VC, c = cx < a.d - VC ? cx : a.d - VC;
+    if (cx >= a.d) return;
     const long long row = blockIdx.x;
     const int slot = a.slots ? a.slots[row] : (int)row;
     S *y = (S *)a.y + row * a.d + c;
+    float out[VC] = {};
     if (slot < 0 || slot >= a.pool) {
-        *y = E::from(0.0f);
+        store_vec<E, VC>(y, VC, out);
         return;
     }
-    const RecurChannel ch(a.A, a.r_bias, a.i_bias, c);
-    float *state = a.state + (long long)slot * a.d + c;
-    const float x = E::to(((const S *)a.x)[row * a.x_row + c]), r = E::to(((const S *)a.r)[row * a.r_row + c]);
-    const float i = E::to(((const S *)a.i)[row * a.i_row + c]);
-    const float L = ch.A * sigmoid_f32(r + ch.rb), dec = __builtin_amdgcn_exp2f(L * kLog2e);
-    const float h = fmaf(dec, *state, __builtin_amdgcn_sqrtf(one_minus_square(L, dec)) * sigmoid_f32(i + ch.ib) * x);
-    *state = h;
-    float out = h;
-    if (a.z) {
-        const float z = E::to(((const S *)a.z)[row * a.z_row + c]);
-        out = h * (z * sigmoid_f32(z));
+    const RecurChannels<VC> ch(a.A, a.r_bias, a.i_bias, c);
+    float h[VC], x[VC], r[VC], i[VC], z[VC];
+    load_vec<E, VC>((const S *)a.x + row * a.x_row + c, VC, x);
+    load_vec<E, VC>((const S *)a.r + row * a.r_row + c, VC, r);
+    load_vec<E, VC>((const S *)a.i + row * a.i_row + c, VC, i);
+    if (a.z) load_vec<E, VC>((const S *)a.z + row * a.z_row + c, VC, z);
+    recur_get<VC>(a.state, slot, a.d, c, h);
+#pragma unroll
+    for (int v = 0; v < VC; ++v) {
+        const float L = ch.A[v] * recur_gate(r[v], ch.rb[v]), dec = __builtin_amdgcn_exp2f(L);
+        h[v] = fmaf(dec, h[v], __builtin_amdgcn_sqrtf(one_minus_square(L, dec)) * recur_gate(i[v], ch.ib[v]) * x[v]);
+        out[v] = a.z ? h[v] * (z[v] * sigmoid_f32(z[v])) : h[v];
     }
-    *y = E::from(out);
+    if (c == cx) {
+        recur_put<VC>(a.state, slot, a.d, c, h);
+        store_vec<E, VC>(y, VC, out);
+    } else {
+#pragma unroll
+        for (int v = 1; v < VC; ++v)
+            if (c + v >= cx) {
+                a.state[(long long)slot * a.d + c + v] = h[v];
+                y[v] = E::from(out[v]);
+            }
+    }
 }
 
-template <class E>
-hipError_t launch(const RecurArgs &a, hipStream_t st)
+template <class E, int VC, int LC>
+hipError_t launch_shape(const RecurArgs &a, hipStream_t st)
 {
-    const unsigned by = (unsigned)((a.d + kRecurChannels - 1) / kRecurChannels);
-    if (a.joined && a.chunks > 1) {
-        recur_kernel<E, true><<<dim3((unsigned)a.chunks - 1, by), 64 * kRecurWaves, 0, st>>>(a);
+    if (a.joined) {
+        const unsigned blocks = (unsigned)((a.chunks - a.tail) * a.across);
+        recur_kernel<E, VC, LC, true, false><<<(blocks + 7) / 8 * 8, 64 * kRecurWaves, 0, st>>>(a);
         if (hipError_t e = hipGetLastError()) return e;
     }
-    const unsigned states = a.final_state ? (unsigned)((a.q.seqs + kRecurStateSeqs - 1) / kRecurStateSeqs) : 0;
-    recur_kernel<E, false><<<dim3((unsigned)a.chunks + states, by), 64 * kRecurWaves, 0, st>>>(a);
+    const unsigned blocks = (unsigned)(a.chunks * a.across), states = a.final_state ? (unsigned)((a.q.seqs + kRecurStateSeqs - 1) / kRecurStateSeqs) : 0;
+    const unsigned grid = (blocks + 7) / 8 * 8 + states * a.across;
+    if (a.z) recur_kernel<E, VC, LC, false, true><<<grid, 64 * kRecurWaves, 0, st>>>(a);
+    else recur_kernel<E, VC, LC, false, false><<<grid, 64 * kRecurWaves, 0, st>>>(a);
     return hipGetLastError();
+}
+template <class E>
+hipError_t launch(const RecurArgs &a, const RecurShape &s, hipStream_t st)
+{
+    return recur_by_shape<E>(s, [&](auto vc, auto lc) { return launch_shape<E, decltype(vc)::value, decltype(lc)::value>(a, st); });
 }
 
 }  // namespace
 
-hipError_t launch_recurrence(int dtype, const RecurArgs &a, hipStream_t st)
+hipError_t launch_recurrence(int dtype, const RecurArgs &a, const RecurShape &s, hipStream_t st)
 {
     switch (dtype) {
-        case CONV2D_DTYPE_F16: return launch<SF16>(a, st);
-        case CONV2D_DTYPE_BF16: return launch<SBF16>(a, st);
-        default: return launch<SF32>(a, st);
+        case CONV2D_DTYPE_F16: return launch<SF16>(a, s, st);
+        case CONV2D_DTYPE_BF16: return launch<SBF16>(a, s, st);
+        default: return launch<SF32>(a, s, st);
     }
+}
+
+template <class E>
+static hipError_t launch_step(const RecurStepArgs &a, hipStream_t st)
+{
+    constexpr int VC = kRecurStepChannels;
+    if (a.d < VC) recur_step_kernel<E, 1><<<(unsigned)a.rows, 256, 0, st>>>(a);
+    else recur_step_kernel<E, VC><<<dim3((unsigned)a.rows, (unsigned)((a.d + 256 * VC - 1) / (256 * VC))), 256, 0, st>>>(a);
+    return hipGetLastError();
 }
 
 hipError_t launch_recurrence_step(int dtype, const RecurStepArgs &a, hipStream_t st)
 {
-    const dim3 grid((unsigned)a.rows, (unsigned)((a.d + 255) / 256));
     switch (dtype) {
-        case CONV2D_DTYPE_F16: recur_step_kernel<SF16><<<grid, 256, 0, st>>>(a); break;
-        case CONV2D_DTYPE_BF16: recur_step_kernel<SBF16><<<grid, 256, 0, st>>>(a); break;
-        default: recur_step_kernel<SF32><<<grid, 256, 0, st>>>(a); break;
+        case CONV2D_DTYPE_F16: return launch_step<SF16>(a, st);
+        case CONV2D_DTYPE_BF16: return launch_step<SBF16>(a, st);
+        default: return launch_step<SF32>(a, st);
     }
-    return hipGetLastError();
 }
 
 }  // namespace cnv

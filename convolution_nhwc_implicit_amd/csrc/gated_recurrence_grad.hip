@@ -17,332 +17,380 @@
 namespace cnv {
 namespace {
 
-struct Token {
-    float g, u, L, a, x;
-    template <class E>
-    __device__ static inline Token of(const RecurChannel &ch, E, float r, float i, float x)
-    {
-        Token k;
-        k.g = sigmoid_f32(r + ch.rb);
-        k.u = sigmoid_f32(i + ch.ib);
-        k.L = ch.A * k.g;
-        k.a = __builtin_amdgcn_exp2f(k.L * kLog2e);
-        k.x = x;
-        return k;
-    }
-};
-
-// A run's values as they lie in memory.
-template <class E, int T>
-struct Loads {
-    typename E::S x[T], r[T], i[T], z[T], dy[T];
-};
-template <class E>
+template <class E, int VC>
 struct Tensors {
-    RecurRows<E> x, r, i, z, dy;
-    bool gate;
-    __device__ inline Tensors(const RecurArgs &a, const RecurChunk &k, int c)
-        : x(a.x, a.xs, k, a.q.len, a.per_seq, c), r(a.r, a.rs, k, a.q.len, a.per_seq, c), i(a.i, a.is, k, a.q.len, a.per_seq, c),
-          z(a.z, a.zs, k, a.q.len, a.per_seq, c), dy(a.dy, a.dys, k, a.q.len, a.per_seq, c), gate(a.z != nullptr)
+    RecurRows<E, VC> x, r, i, z, dy;
+    template <class Place>
+    __device__ inline Tensors(const RecurArgs &a, const RecurChunk &k, const Place &at)
+        : x(a.x, a.xs, a, k, at), r(a.r, a.rs, a, k, at), i(a.i, a.is, a, k, at), z(a.z, a.zs, a, k, at), dy(a.dy, a.dys, a, k, at)
     {
     }
-    template <bool BACK, int T>
-    __device__ inline void load(const RecurRun<T> &run, Loads<E, T> &v) const
-    {
-        x.load(run, v.x);
-        r.load(run, v.r);
-        i.load(run, v.i);
-        if (BACK) {
-            dy.load(run, v.dy);
-            if (gate) z.load(run, v.z);
-        }
-    }
 };
-
-// What a run does to a state, and to the gradient that flows back through it.
-struct Piece {
-    float dec = 1.0f, end = 0.0f, bdec = 1.0f, flow = 0.0f;
-};
-template <int T>
-__device__ inline void state_piece(const RecurArgs &a, const RecurRun<T> &run, int c, const float (&av)[T], const float (&bv)[T], Piece &p)
-{
-    if (run.f == 0) {
-#pragma unroll
-        for (int j = 0; j < T; ++j) {
-            p.dec *= av[j];
-            p.end = fmaf(av[j], p.end, bv[j]);
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < T; ++j) {
-            if (run.f >> j & 1) {
-                p.dec = -1.0f;
-                p.end = a.initial ? a.initial[(long long)a.q.find(run.t0 + j) * a.d + c] : 0.0f;
-            }
-            p.dec = p.dec < 0.0f ? p.dec : p.dec * av[j];
-            p.end = fmaf(av[j], p.end, bv[j]);
-        }
-    }
-}
-template <int T>
-__device__ inline float final_gradient(const RecurArgs &a, const RecurRun<T> &run, int c, int j)
-{
-    return a.dfinal ? a.dfinal[(long long)a.q.find(run.t0 + j) * a.d + c] : 0.0f;
-}
-template <int T>
-__device__ inline void flow_piece(const RecurArgs &a, const RecurRun<T> &run, int c, const float (&av)[T], const float (&G)[T], Piece &p)
-{
-    if (run.last == 0) {
-#pragma unroll
-        for (int j = T - 1; j >= 0; --j) {
-            p.flow = av[j] * (p.flow + G[j]);
-            p.bdec *= av[j];
-        }
-    } else {
-#pragma unroll
-        for (int j = T - 1; j >= 0; --j) {
-            if (run.last >> j & 1) {
-                p.bdec = -1.0f;
-                p.flow = final_gradient(a, run, c, j);
-            }
-            p.flow = av[j] * (p.flow + G[j]);
-            p.bdec = p.bdec < 0.0f ? p.bdec : p.bdec * av[j];
-        }
-    }
-}
-// tokens that are not there: nothing decays, nothing comes in
-template <int T>
-__device__ inline void cut_run(const RecurRun<T> &run, float (&av)[T], float (&in)[T])
-{
-    if (run.n < T)
-#pragma unroll
-        for (int j = 0; j < T; ++j) {
-            av[j] = j < run.n ? av[j] : 1.0f;
-            in[j] = j < run.n ? in[j] : 0.0f;
-        }
-}
 
 // The first walk.  BACK: sequences may go on in another chunk, which needs the
 // gradient's flow through this one.
-template <class E, bool BACK>
-__global__ __launch_bounds__(64 * kRecurGradWaves) void recur_states_kernel(RecurArgs a)
+template <class E, int VC, int LC, bool BACK>
+__global__ __launch_bounds__(64 * kRecurWaves) void recur_states_kernel(RecurArgs a)
 {
-    constexpr int T = kRecurGradRun, W = kRecurGradWaves;
+    constexpr int T = kRecurRun, W = kRecurWaves;
+    typedef RecurPlace<VC, LC, T> Place;
+    constexpr int kSegment = W * Place::kSpan;
     __shared__ uint32_t bits[RecurChunk::kWords];
-    __shared__ float ends[2][BACK ? 4 : 2][W][64];
-    const int lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64);
-    const int cx = blockIdx.y * kRecurChannels + lane, c = cx < a.d ? cx : a.d - 1;
-    const bool mine = cx < a.d;
-    const RecurChunk chunk(a, bits, blockIdx.x);
-    const RecurChannel ch(a.A, a.r_bias, a.i_bias, c);
-    const Tensors<E> in(a, chunk, c);
-    float decay = 1.0f, state = 0.0f, bdecay = 1.0f, flow = 0.0f;
-    long long seg = (long long)blockIdx.x * (a.chunk / (T * W));
-    Loads<E, T> v;
-    if (chunk.len > 0) in.template load<BACK>(RecurRun<T>(chunk, wave * T), v);
-    for (int at0 = 0, buf = 0; at0 < chunk.len; at0 += T * W, buf ^= 1, ++seg) {
-        const RecurRun<T> run(chunk, at0 + wave * T);
-        if (wave == 0 && mine) {
-            a.seg_decay[seg * a.d + c] = decay;
-            a.seg_state[seg * a.d + c] = state;
+    __shared__ float2 ends[2][BACK ? 2 : 1][W][LC * VC];
+    typedef RecurRaw<E, VC> Raw;
+    const int blocks = a.chunks * a.across, id = recur_block(blockIdx.x, blocks);
+    if (id >= blocks) return;
+    const int index = id / a.across;
+    const Place at(id % a.across, a.d);
+    RecurChunk chunk(a, bits, index);
+    const RecurChannels<VC> ch(a.A, a.r_bias, a.i_bias, at.c);
+    const Tensors<E, VC> in(a, chunk, at);
+    const bool gate = BACK && a.z;
+    float state[VC] = {};
+    RecurPiece<VC> total, back;
+    total.clear();
+    back.clear();
+    const int lead = at.wave * Place::kSpan;
+    Raw xs[T], rs[T], is[T], zs[T], ds[T];
+    struct {
+        __amdgpu_buffer_rsrc_t x, r, i, z, dy;
+    } next;
+    auto aim = [&](const RecurSpan &span) {
+        next.x = in.x.span(span);
+        next.r = in.r.span(span);
+        next.i = in.i.span(span);
+        if (BACK) {
+            next.dy = in.dy.span(span);
+            next.z = in.z.span(span);
         }
-        float av[T], bv[T], G[T];
+    };
+    auto load = [&](int j, auto inside) {
+        constexpr bool INSIDE = decltype(inside)::value;
+        in.r.template load<INSIDE>(next.r, j, rs[j]);
+        in.i.template load<INSIDE>(next.i, j, is[j]);
+        in.x.template load<INSIDE>(next.x, j, xs[j]);
+        if (BACK) {
+            in.dy.template load<INSIDE>(next.dy, j, ds[j]);
+            in.z.template load<INSIDE>(next.z, j, zs[j]);
+        }
+    };
+    aim(RecurSpan(chunk, at, lead));
+#pragma unroll
+    for (int j = 0; j < T; ++j) load(j, std::false_type{});
+    chunk.mark(a);
+    // INSIDE: this segment lies inside a sequence, and all of the next one's tokens are there
+    auto segment = [&](int seg, auto inside) {
+        constexpr bool INSIDE = decltype(inside)::value;
+        const int buf = seg / kSegment & 1;
+        if (at.wave == 0 && at.q == 0 && at.mine) {
+            const long long k = (long long)index * (a.chunk / kSegment) + seg / kSegment;
+            recur_put<VC>(a.seg_decay, k, a.d, at.c, total.dec);
+            recur_put<VC>(a.seg_state, k, a.d, at.c, state);
+        }
+        const RecurSpan span(chunk, at, seg + lead);
+        const RecurRun<T> run = INSIDE ? RecurRun<T>() : RecurRun<T>(chunk, at, span);
+        aim(RecurSpan(chunk, at, seg + lead + kSegment));
+        float av[T][VC], bv[T][VC], gv[T][VC];
 #pragma unroll
         for (int j = 0; j < T; ++j) {
-            const Token k = Token::of(ch, E{}, E::to(v.r[j]), E::to(v.i[j]), E::to(v.x[j]));
-            av[j] = k.a;
-            bv[j] = __builtin_amdgcn_sqrtf(one_minus_square(k.L, k.a)) * k.u * k.x;
-            if (BACK) {
-                G[j] = E::to(v.dy[j]);
-                if (in.gate) {
-                    const float z = E::to(v.z[j]);
-                    G[j] *= z * sigmoid_f32(z);
+#pragma unroll
+            for (int v = 0; v < VC; ++v) {
+                const float L = ch.A[v] * recur_gate(rs[j][v], ch.rb[v]);
+                av[j][v] = __builtin_amdgcn_exp2f(L);
+                bv[j][v] = __builtin_amdgcn_sqrtf(one_minus_square(L, av[j][v])) * recur_gate(is[j][v], ch.ib[v]) * xs[j][v];
+                if (BACK) {
+                    const float z = zs[j][v];
+                    gv[j][v] = gate ? ds[j][v] * (z * sigmoid_f32(z)) : ds[j][v];
                 }
             }
+            load(j, inside);
         }
-        in.template load<BACK>(RecurRun<T>(chunk, at0 + T * W + wave * T), v);
-        cut_run(run, av, bv);
-        Piece p;
-        state_piece(a, run, c, av, bv, p);
-        if constexpr (BACK) {
-            cut_run(run, av, G);
-            flow_piece(a, run, c, av, G, p);
+        if (!INSIDE) {
+            recur_cut<VC, T>(run, bv);
+            if (BACK) recur_cut<VC, T>(run, gv);
         }
-        ends[buf][0][wave][lane] = p.dec;
-        ends[buf][1][wave][lane] = p.end;
+        const long long t0 = chunk.c0 + seg + lead + at.q * T;
+        if (!INSIDE && run.firsts && a.initial)
+            recur_gather<VC, T>(a, a.initial, run.f, t0, at.c, [&](int j, const float (&h)[VC]) {
+#pragma unroll
+                for (int v = 0; v < VC; ++v) bv[j][v] = fmaf(av[j][v], h[v], bv[j][v]);
+            });
+        RecurPiece<VC> p;
+        recur_piece<VC, T>(run.f, run.firsts, av, bv, p);
+        RecurJoin<VC, LC, W, false, INSIDE> join(p, at);
+        join.put(ends[buf][0]);
         if constexpr (BACK) {
-            ends[buf][2][wave][lane] = p.bdec;
-            ends[buf][3][wave][lane] = p.flow;
+            if (!INSIDE && run.lasts && a.dfinal)
+                recur_gather<VC, T>(a, a.dfinal, run.last, t0, at.c, [&](int j, const float (&k)[VC]) {
+#pragma unroll
+                    for (int v = 0; v < VC; ++v) gv[j][v] += k[v];
+                });
+            RecurPiece<VC> flow;
+            recur_flow<VC, T>(run.last, run.lasts, av, gv, flow);
+            RecurJoin<VC, LC, W, true, INSIDE>(flow, at).put(ends[buf][1]);
         }
         __syncthreads();
-#pragma unroll
-        for (int w = 0; w < W; ++w) {
-            const float d = ends[buf][0][w][lane];
-            state = through(d, ends[buf][1][w][lane], state);
-            decay = joined_decay(decay, d);
-            if constexpr (BACK) {
-                if (bdecay >= 0.0f) flow = fmaf(bdecay, ends[buf][3][w][lane], flow);
-                bdecay = joined_decay(bdecay, ends[buf][2][w][lane]);
+        float h[VC];
+        join.get(ends[buf][0], state, h, &total);
+        if constexpr (BACK) {  // the segment's flow, behind the chunk's so far
+#pragma unroll 4
+            for (int w = W - 1; w >= 0; --w) {
+                RecurPiece<VC> s;
+                s.get(&ends[buf][1][w][at.slot]);
+                back.template after<false>(s);
             }
         }
+    };
+    for (int seg = 0, begin = 0; seg < chunk.len; seg += kSegment) {
+        while (begin < seg) begin = chunk.next(seg, a.chunk);
+        if (begin > seg + kSegment && seg + 2 * kSegment <= chunk.len) segment(seg, std::true_type{});
+        else segment(seg, std::false_type{});
     }
-    if (BACK && wave == 0 && mine) {
-        const long long at = (long long)blockIdx.x * a.d + c;
-        a.chunk_decay[at] = decay;
-        a.chunk_state[at] = state;
-        a.back_decay[at] = bdecay;
-        a.chunk_back[at] = flow;
+    if (BACK && at.wave == 0 && at.q == 0 && at.mine) {
+        recur_put<VC>(a.chunk_decay, index, a.d, at.c, total.dec);
+        recur_put<VC>(a.chunk_state, index, a.d, at.c, state);
+        recur_put<VC>(a.back_decay, index, a.d, at.c, back.dec);
+        recur_put<VC>(a.chunk_back, index, a.d, at.c, back.end);
     }
 }
 
-template <class E>
-__global__ __launch_bounds__(64 * kRecurGradWaves) void recur_grad_kernel(RecurArgs a)
+template <class E, int VC, int LC>
+__global__ __launch_bounds__(64 * kRecurWaves) void recur_grad_kernel(RecurArgs a)
 {
-    constexpr int T = kRecurGradRun, W = kRecurGradWaves;
+    constexpr int T = kRecurRun, W = kRecurWaves;
+    typedef RecurPlace<VC, LC, T> Place;
+    constexpr int kSegment = W * Place::kSpan;
     __shared__ uint32_t bits[RecurChunk::kWords];
-    __shared__ float ends[2][4][W][64];
-    using S = typename E::S;
-    const int lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64);
-    const int cx = blockIdx.y * kRecurChannels + lane, c = cx < a.d ? cx : a.d - 1;
-    const bool mine = cx < a.d;
-    if ((int)blockIdx.x >= a.chunks) {  // initial states of empty sequences
-        const long long s0 = (long long)(blockIdx.x - a.chunks) * kRecurStateSeqs;
-        for (long long s = s0 + wave; s < s0 + kRecurStateSeqs && s < a.q.seqs; s += W)
-            if (mine && a.q.begin((int)s) == a.q.end((int)s))
-                a.dinitial[s * a.d + c] = a.dfinal ? a.dfinal[s * a.d + c] : 0.0f;
+    __shared__ float2 ends[2][2][W][LC * VC];
+    typedef RecurRaw<E, VC> Raw;
+    const int blocks = a.chunks * a.across, id = recur_block(blockIdx.x, blocks);
+    if ((int)blockIdx.x >= (blocks + 7) / 8 * 8) {  // initial states of empty sequences
+        const int b = blockIdx.x - (blocks + 7) / 8 * 8;
+        const Place at(b % a.across, a.d);
+        const long long s0 = (long long)(b / a.across) * kRecurStateSeqs;
+        for (long long s = s0 + at.wave; s < s0 + kRecurStateSeqs && s < a.q.seqs; s += W)
+            if (at.mine && at.q == 0 && a.q.begin((int)s) == a.q.end((int)s)) {
+                float k[VC] = {};
+                if (a.dfinal) recur_get<VC>(a.dfinal, s, a.d, at.c, k);
+                recur_put<VC>(a.dinitial, s, a.d, at.c, k);
+            }
         return;
     }
-    const RecurChunk chunk(a, bits, blockIdx.x);
-    const RecurChannel ch(a.A, a.r_bias, a.i_bias, c);
-    const Tensors<E> in(a, chunk, c);
-    float before = 0.0f, flow = 0.0f;  // the state the chunk starts with; the gradient that flows in behind it
+    if (id >= blocks) return;
+    const int index = id / a.across;
+    const Place at(id % a.across, a.d);
+    RecurChunk chunk(a, bits, index);
+    const RecurChannels<VC> ch(a.A, a.r_bias, a.i_bias, at.c);
+    const Tensors<E, VC> in(a, chunk, at);
+    const RecurOut<E, VC> dxr(a.dx, a, chunk, at), drr(a.dr, a, chunk, at), dir(a.di, a, chunk, at), dzr(a.dz, a, chunk, at);
+    const bool gate = a.z;
+    float invA[VC], dll[VC] = {}, drb[VC] = {}, dib[VC] = {};
+#pragma unroll
+    for (int v = 0; v < VC; ++v) invA[v] = ch.A[v] == 0.0f ? 0.0f : 1.0f / ch.A[v];
+    const int segs = (chunk.len + kSegment - 1) / kSegment;
+    Raw xs[T], rs[T], is[T], zs[T], ds[T];
+    struct {
+        __amdgpu_buffer_rsrc_t x, r, i, z, dy;
+    } next;
+    auto aim = [&](const RecurSpan &span) {
+        next.x = in.x.span(span);
+        next.r = in.r.span(span);
+        next.i = in.i.span(span);
+        next.dy = in.dy.span(span);
+        next.z = in.z.span(span);
+    };
+    auto load = [&](int j, auto inside) {
+        constexpr bool INSIDE = decltype(inside)::value;
+        in.r.template load<INSIDE>(next.r, j, rs[j]);
+        in.i.template load<INSIDE>(next.i, j, is[j]);
+        in.x.template load<INSIDE>(next.x, j, xs[j]);
+        in.dy.template load<INSIDE>(next.dy, j, ds[j]);
+        in.z.template load<INSIDE>(next.z, j, zs[j]);
+    };
+    const int lead = at.wave * Place::kSpan;
+    aim(RecurSpan(chunk, at, (segs > 0 ? segs - 1 : 0) * kSegment + lead));
+#pragma unroll
+    for (int j = 0; j < T; ++j) load(j, std::false_type{});
+    chunk.mark(a);
+    float start[VC] = {}, flow[VC] = {};  // the state the chunk starts with; the gradient that flows in behind it
     if (a.joined) {
         const int after = a.per_seq ? chunk.before + a.per_seq : a.chunks;
-        for (int k = chunk.before; k < (int)blockIdx.x; ++k)
-            before = through(a.chunk_decay[(long long)k * a.d + c], a.chunk_state[(long long)k * a.d + c], before);
-        for (int k = after - 1; k > (int)blockIdx.x; --k)
-            flow = through(a.back_decay[(long long)k * a.d + c], a.chunk_back[(long long)k * a.d + c], flow);
+#pragma unroll 4
+        for (int k = chunk.before; k < index; ++k) {
+            RecurPiece<VC> p;
+            recur_get<VC>(a.chunk_decay, k, a.d, at.c, p.dec);
+            recur_get<VC>(a.chunk_state, k, a.d, at.c, p.end);
+            p.template carry<false>(start);
+        }
+#pragma unroll 4
+        for (int k = after - 1; k > index; --k) {
+            RecurPiece<VC> p;
+            recur_get<VC>(a.back_decay, k, a.d, at.c, p.dec);
+            recur_get<VC>(a.chunk_back, k, a.d, at.c, p.end);
+            p.template carry<false>(flow);
+        }
     }
-    float dll = 0.0f, drb = 0.0f, dib = 0.0f;
-    const int segs = (chunk.len + T * W - 1) / (T * W);
-    Loads<E, T> v;
-    if (segs > 0) in.template load<true>(RecurRun<T>(chunk, ((segs - 1) * W + wave) * T), v);
-    for (int sg = segs - 1, buf = 0; sg >= 0; --sg, buf ^= 1) {
-        const RecurRun<T> run(chunk, (sg * W + wave) * T);
-        float xv[T], gv[T], uv[T], Lv[T], av[T], bv[T], wv[T], zv[T], dv[T], G[T];
+    // INSIDE: this segment lies inside a sequence, and another one is before it
+    auto segment = [&](int seg, auto inside) {
+        constexpr bool INSIDE = decltype(inside)::value;
+        const int buf = seg / kSegment & 1;
+        const RecurSpan span(chunk, at, seg + lead);
+        const RecurRun<T> run = INSIDE ? RecurRun<T>() : RecurRun<T>(chunk, at, span);
+        const long long t0 = chunk.c0 + seg + lead + at.q * T, k0 = (long long)index * (a.chunk / kSegment) + seg / kSegment;
+        RecurPiece<VC> until;  // the chunk before this segment
+        recur_get<VC>(a.seg_decay, k0, a.d, at.c, until.dec);
+        recur_get<VC>(a.seg_state, k0, a.d, at.c, until.end);
+        aim(RecurSpan(chunk, at, seg > 0 ? seg + lead - kSegment : segs * kSegment));
+        // su: sqrt(1 - a^2) u; hv: the inputs, then the states before the tokens; qv: dz by h
+        float Lv[T][VC], av[T][VC], su[T][VC], hv[T][VC], gv[T][VC], qv[T][VC];
+        Raw x[T];
 #pragma unroll
         for (int j = 0; j < T; ++j) {
-            const Token k = Token::of(ch, E{}, E::to(v.r[j]), E::to(v.i[j]), E::to(v.x[j]));
-            xv[j] = k.x;
-            gv[j] = k.g;
-            uv[j] = k.u;
-            Lv[j] = k.L;
-            av[j] = k.a;
-            wv[j] = one_minus_square(k.L, k.a);
-            bv[j] = __builtin_amdgcn_sqrtf(wv[j]) * k.u * k.x;
-            dv[j] = E::to(v.dy[j]);
-            zv[j] = 0.0f;
-            G[j] = dv[j];
-            if (in.gate) {
-                zv[j] = E::to(v.z[j]);
-                G[j] *= zv[j] * sigmoid_f32(zv[j]);
+            x[j] = xs[j];
+#pragma unroll
+            for (int v = 0; v < VC; ++v) {
+                Lv[j][v] = ch.A[v] * recur_gate(rs[j][v], ch.rb[v]);
+                av[j][v] = __builtin_amdgcn_exp2f(Lv[j][v]);
+                su[j][v] = __builtin_amdgcn_sqrtf(one_minus_square(Lv[j][v], av[j][v])) * recur_gate(is[j][v], ch.ib[v]);
+                hv[j][v] = su[j][v] * x[j][v];
+                const float dy = ds[j][v];
+                const float z = zs[j][v], s = sigmoid_f32(z);
+                gv[j][v] = gate ? dy * (z * s) : dy;
+                qv[j][v] = dy * (s * (1.0f + z * (1.0f - s)));
             }
+            load(j, inside);
         }
-        if (sg > 0) in.template load<true>(RecurRun<T>(chunk, ((sg - 1) * W + wave) * T), v);
-        cut_run(run, av, bv);
-        cut_run(run, av, G);
-        Piece p;
-        state_piece(a, run, c, av, bv, p);
-        flow_piece(a, run, c, av, G, p);
-        ends[buf][0][wave][lane] = p.dec;
-        ends[buf][1][wave][lane] = p.end;
-        ends[buf][2][wave][lane] = p.bdec;
-        ends[buf][3][wave][lane] = p.flow;
+        if (!INSIDE) {
+            recur_cut<VC, T>(run, hv);
+            recur_cut<VC, T>(run, gv);
+        }
+        if (!INSIDE && run.firsts && a.initial)
+            recur_gather<VC, T>(a, a.initial, run.f, t0, at.c, [&](int j, const float (&h)[VC]) {
+#pragma unroll
+                for (int v = 0; v < VC; ++v) hv[j][v] = fmaf(av[j][v], h[v], hv[j][v]);
+            });
+        if (!INSIDE && run.lasts && a.dfinal)
+            recur_gather<VC, T>(a, a.dfinal, run.last, t0, at.c, [&](int j, const float (&k)[VC]) {
+#pragma unroll
+                for (int v = 0; v < VC; ++v) gv[j][v] += k[v];
+            });
+        RecurPiece<VC> p;
+        recur_piece<VC, T>(run.f, run.firsts, av, hv, p);
+        RecurJoin<VC, LC, W, false, INSIDE> states(p, at);
+        states.put(ends[buf][0]);
+        recur_flow<VC, T>(run.last, run.lasts, av, gv, p);
+        RecurJoin<VC, LC, W, true, INSIDE> flows(p, at);
+        flows.put(ends[buf][1]);
         __syncthreads();
-        const long long seg = (long long)blockIdx.x * (a.chunk / (T * W)) + sg;
-        float h = through(a.seg_decay[seg * a.d + c], a.seg_state[seg * a.d + c], before);
-        float k = flow;
+        float h[VC], k[VC], begin[VC];
 #pragma unroll
-        for (int w = 0; w < W; ++w)
-            if (w < wave) h = through(ends[buf][0][w][lane], ends[buf][1][w][lane], h);
+        for (int v = 0; v < VC; ++v) begin[v] = start[v];
+        until.template carry<false>(begin);
+        states.get(ends[buf][0], begin, h, nullptr);
+        flows.get(ends[buf][1], flow, k, nullptr);
 #pragma unroll
-        for (int w = W - 1; w >= 0; --w) {
-            flow = through(ends[buf][2][w][lane], ends[buf][3][w][lane], flow);
-            if (w > wave) k = flow;
-        }
-        float hv[T];  // the states before each token
+        for (int j = 0; j < T; ++j)
 #pragma unroll
-        for (int j = 0; j < T; ++j) {
-            if (run.f >> j & 1) h = a.initial ? a.initial[(long long)a.q.find(run.t0 + j) * a.d + c] : 0.0f;
-            hv[j] = h;
-            h = fmaf(av[j], h, bv[j]);
-        }
+            for (int v = 0; v < VC; ++v) {
+                if (!INSIDE) h[v] = run.f >> j & 1 ? 0.0f : h[v];
+                const float b = hv[j][v];
+                hv[j][v] = h[v];
+                h[v] = fmaf(av[j][v], h[v], b);
+            }
+        if (!INSIDE && run.firsts && a.initial)
+            recur_gather<VC, T>(a, a.initial, run.f, t0, at.c, [&](int j, const float (&h0)[VC]) {
+#pragma unroll
+                for (int v = 0; v < VC; ++v) hv[j][v] = h0[v];
+            });
+        if (!INSIDE) recur_cut<VC, T>(run, hv);  // nothing times nothing for the sums, also behind a spoilt state
+        const __amdgpu_buffer_rsrc_t dx = dxr.span(span), dr = drr.span(span), di = dir.span(span), dz = dzr.span(span);
 #pragma unroll
         for (int j = T - 1; j >= 0; --j) {
-            if (j >= run.n) continue;
-            if (run.last >> j & 1) k = final_gradient(a, run, c, j);
-            const float root = __builtin_amdgcn_rsqf(fmaxf(wv[j], 1.2e-38f)), size = wv[j] * root;
-            const float in_ = uv[j] * xv[j], hj = fmaf(av[j], hv[j], bv[j]);
-            float dz = 0.0f;
-            if (in.gate) {
-                const float s = sigmoid_f32(zv[j]);
-                dz = dv[j] * hj * (s * (1.0f + zv[j] * (1.0f - s)));
+            float ox[VC], orr[VC], oi[VC], oz[VC];
+#pragma unroll
+            for (int v = 0; v < VC; ++v) {
+                const float L = Lv[j][v], dec = av[j][v], xx = x[j][v], b = su[j][v] * xx;
+                // 1 / sqrt(1 - a^2), finite where a is 1: it meets L or b there, which are 0
+                const float root = __builtin_amdgcn_rsqf(fmaxf(one_minus_square(L, dec), 1.2e-38f)), u = su[j][v] * root;
+                if (!INSIDE) k[v] = run.last >> j & 1 ? 0.0f : k[v];
+                k[v] += gv[j][v];
+                const float dl = kLn2 * k[v] * (L * dec * hv[j][v] - (L * root) * (dec * dec) * (u * xx));  // dL * L
+                orr[v] = dl * (1.0f - L * invA[v]);
+                oi[v] = k[v] * b * (1.0f - u);
+                ox[v] = k[v] * su[j][v];
+                oz[v] = qv[j][v] * fmaf(dec, hv[j][v], b);
+                dll[v] += dl;
+                drb[v] += orr[v];
+                dib[v] += oi[v];
+                k[v] *= dec;
+                gv[j][v] = k[v];
             }
-            k += G[j];
-            const float dl = k * (av[j] * hv[j] * Lv[j] - av[j] * av[j] * in_ * (Lv[j] * root));  // dL * L
-            const float dr = dl * (1.0f - gv[j]), di = k * bv[j] * (1.0f - uv[j]);
-            dll += dl;
-            drb += dr;
-            dib += di;
-            if (mine) {
-                const long long at = (run.t0 + j) * a.d + c;
-                ((S *)a.dx)[at] = E::from(k * size * uv[j]);
-                ((S *)a.dr)[at] = E::from(dr);
-                ((S *)a.di)[at] = E::from(di);
-                if (in.gate) ((S *)a.dz)[at] = E::from(dz);
-            }
-            k *= av[j];
-            if ((run.f >> j & 1) && a.dinitial && mine) a.dinitial[(long long)a.q.find(run.t0 + j) * a.d + c] = k;
+            dxr.template store<INSIDE>(dx, j, ox);
+            drr.template store<INSIDE>(dr, j, orr);
+            dir.template store<INSIDE>(di, j, oi);
+            dzr.template store<INSIDE>(dz, j, oz);
+            __builtin_amdgcn_sched_barrier(0);  // a token's roots, worked out for all of them at once, would spill
+        }
+        if (!INSIDE && run.firsts && a.dinitial) recur_scatter<VC, T>(a, run.f, t0, at, gv, a.dinitial);
+    };
+    for (int sg = segs - 1; sg >= 0; --sg) {
+        // whether a sequence begins in it or right behind it, or tokens are missing
+        const int seg = sg * kSegment;
+        if (sg > 0 && seg + kSegment <= chunk.len && chunk.next(seg, a.chunk) > seg + kSegment) segment(seg, std::true_type{});
+        else segment(seg, std::false_type{});
+    }
+    // the sums of a wave's groups, then the waves' in order
+    __syncthreads();
+    float *sums = (float *)ends;
+    static_assert(sizeof(ends) >= sizeof(float) * W * 3 * LC * VC, "room for the sums");
+#pragma unroll
+    for (int v = 0; v < VC; ++v) {
+        float s[3] = {dll[v], drb[v], dib[v]};
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+#pragma unroll
+            for (int o = LC; o < 64; o *= 2) s[i] += __shfl_xor(s[i], o);
+            if (at.q == 0) sums[(at.wave * 3 + i) * LC * VC + at.slot + v] = s[i];
         }
     }
-    // the waves' sums in order
     __syncthreads();
-    float *sums = &ends[0][0][0][0];
-    sums[(wave * 3 + 0) * 64 + lane] = dll;
-    sums[(wave * 3 + 1) * 64 + lane] = drb;
-    sums[(wave * 3 + 2) * 64 + lane] = dib;
-    __syncthreads();
-    if (wave < 3 && mine) {
-        float s = 0.0f;
+    if (at.wave < 3 && at.q == 0 && at.mine) {
+        float s[VC] = {};
 #pragma unroll
-        for (int w = 0; w < W; ++w) s += sums[(w * 3 + wave) * 64 + lane];
-        a.partial[((long long)blockIdx.x * 3 + wave) * a.d + c] = s;
+        for (int w = 0; w < W; ++w)
+#pragma unroll
+            for (int v = 0; v < VC; ++v) s[v] += sums[(w * 3 + at.wave) * LC * VC + at.slot + v];
+        recur_put<VC>(a.partial, (long long)index * 3 + at.wave, a.d, at.c, s);
     }
 }
 
-template <class E>
-hipError_t launch(const RecurArgs &a, hipStream_t st)
+template <class E, int VC, int LC>
+hipError_t launch_shape(const RecurArgs &a, hipStream_t st)
 {
-    const unsigned by = (unsigned)((a.d + kRecurChannels - 1) / kRecurChannels);
-    const dim3 grid((unsigned)a.chunks, by);
-    if (a.chunks > 0) {
-        if (a.joined) recur_states_kernel<E, true><<<grid, 64 * kRecurGradWaves, 0, st>>>(a);
-        else recur_states_kernel<E, false><<<grid, 64 * kRecurGradWaves, 0, st>>>(a);
+    const unsigned blocks = ((unsigned)(a.chunks * a.across) + 7) / 8 * 8, threads = 64 * kRecurWaves;
+    if (blocks > 0) {
+        if (a.joined) recur_states_kernel<E, VC, LC, true><<<blocks, threads, 0, st>>>(a);
+        else recur_states_kernel<E, VC, LC, false><<<blocks, threads, 0, st>>>(a);
         if (hipError_t e = hipGetLastError()) return e;
     }
-    const unsigned states = a.dinitial ? (unsigned)((a.q.seqs + kRecurStateSeqs - 1) / kRecurStateSeqs) : 0;
-    if (a.chunks + states > 0) recur_grad_kernel<E><<<dim3((unsigned)a.chunks + states, by), 64 * kRecurGradWaves, 0, st>>>(a);
+    const unsigned states = a.dinitial ? (unsigned)((a.q.seqs + kRecurStateSeqs - 1) / kRecurStateSeqs) * a.across : 0;
+    if (blocks + states > 0) recur_grad_kernel<E, VC, LC><<<blocks + states, threads, 0, st>>>(a);
     return hipGetLastError();
+}
+template <class E>
+hipError_t launch(const RecurArgs &a, const RecurShape &s, hipStream_t st)
+{
+    return recur_by_shape<E>(s, [&](auto vc, auto lc) { return launch_shape<E, decltype(vc)::value, decltype(lc)::value>(a, st); });
 }
 
 }  // namespace
 
-hipError_t launch_recurrence_grad(int dtype, const RecurArgs &a, hipStream_t st)
+hipError_t launch_recurrence_grad(int dtype, const RecurArgs &a, const RecurShape &s, hipStream_t st)
 {
     switch (dtype) {
-        case CONV2D_DTYPE_F16: return launch<SF16>(a, st);
-        case CONV2D_DTYPE_BF16: return launch<SBF16>(a, st);
-        default: return launch<SF32>(a, st);
+        case CONV2D_DTYPE_F16: return launch<SF16>(a, s, st);
+        case CONV2D_DTYPE_BF16: return launch<SBF16>(a, s, st);
+        default: return launch<SF32>(a, s, st);
     }
 }
 

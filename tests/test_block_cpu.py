@@ -167,7 +167,7 @@ def recur(**kw):
     (dict(seqs=0), F16C, INVALID), (dict(tokens=11), F16C, INVALID), (dict(len=-1), F16C, INVALID),
     (dict(r=Stride(-1, 0)), F16C, INVALID), (dict(i=Stride(8, -1)), F16C, INVALID), (dict(z=Stride(1 << 24, 0)), F16C, UNSUPPORTED),
     (dict(seqs=1 << 16, len=1 << 16, tokens=1 << 32), F16C, UNSUPPORTED), (dict(d=1 << 24), F16C, UNSUPPORTED),
-    (dict(d=(1 << 22) - 64), F16C, OK), (dict(d=(1 << 22)), F16C, UNSUPPORTED),  # workgroups along channels: 65535
+    (dict(d=(1 << 24) - 1), F16C, OK),
     (dict(x=Stride(0, 0), r=Stride(0, 0)), F16C, OK), (dict(seqs=1, len=(1 << 31) - 1, tokens=(1 << 31) - 1), F16C, OK),
 ])
 def test_recurrence_abi(kw, dtype, want):
