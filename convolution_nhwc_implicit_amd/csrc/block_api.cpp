@@ -361,19 +361,40 @@ int fp4_quantize(int dtype, int m, int k, const void *x, long long x_row, void *
     return status(launch_fp4_quantize(dtype, a, (hipStream_t)stream));
 }
 
-int fp4_matmul(const fp4_matmul_problem_t *p, int dtype, const void *x, const void *w, const void *w_scale, void *out,
-               void *stream)
+static int check_fp4(const fp4_matmul_problem_t *p, int dtype)
 {
     if (!p || p->m < 0 || p->n < 0 || p->k < 0 || p->x_row < 0) return CONV2D_ERR_INVALID_ARGUMENT;
-    const long long groups = ceil_div(p->k, kFp4Group);
-    if (p->w_pitch < groups * 16) return CONV2D_ERR_INVALID_ARGUMENT;
+    if (p->w_pitch < ceil_div(p->k, kFp4Group) * 16) return CONV2D_ERR_INVALID_ARGUMENT;
     if (!float_type(dtype) || p->w_pitch % 16) return CONV2D_ERR_UNSUPPORTED;
+    // workgroups of up to 512 threads along n and 64 rows along m; the sums' a value to a thread
+    if (ceil_div(p->m, 64) > kMaxGridY || !fits(ceil_div(p->n, 16), 512) || !fits(ceil_div((long long)p->m * p->n, 1024), 256))
+        return CONV2D_ERR_UNSUPPORTED;
+    return CONV2D_OK;
+}
+
+int fp4_matmul_workspace_size(const fp4_matmul_problem_t *prob, int dtype, size_t *bytes)
+{
+    const int r = check_fp4(prob, dtype);
+    if (r != CONV2D_OK) return r;
+    if (!bytes) return CONV2D_ERR_INVALID_ARGUMENT;
+    *bytes = up(fp4_matmul_plan(prob->m, prob->n, prob->k, dtype).bytes(prob->m, prob->n));
+    return CONV2D_OK;
+}
+
+int fp4_matmul(const fp4_matmul_problem_t *p, int dtype, const void *x, const void *w, const void *w_scale, void *out,
+               void *workspace, size_t workspace_bytes, void *stream)
+{
+    const int r = check_fp4(p, dtype);
+    if (r != CONV2D_OK) return r;
     if (p->m == 0 || p->n == 0) return CONV2D_OK;
     if (!out || (p->k > 0 && (!x || !w || !w_scale))) return CONV2D_ERR_INVALID_ARGUMENT;
-    if (!all_aligned(bytes_of(dtype), {x, out}) || !aligned(w, 16)) return CONV2D_ERR_UNSUPPORTED;
-    if (ceil_div(p->m, 64) > kMaxGridY || !fits(ceil_div(p->n, 16), 512)) return CONV2D_ERR_UNSUPPORTED;
-    const Fp4MatmulArgs a = {p->m, p->n, p->k, (int)groups, p->x_row, p->w_pitch, x, (const uint8_t *)w,
-                             (const uint8_t *)w_scale, out};
+    if (!all_aligned(bytes_of(dtype), {x, out}) || !aligned(w, 16) || !aligned(workspace, 16)) return CONV2D_ERR_UNSUPPORTED;
+    const Fp4Plan plan = fp4_matmul_plan(p->m, p->n, p->k, dtype);
+    const size_t need = up(plan.bytes(p->m, p->n));
+    if (need && !workspace) return CONV2D_ERR_INVALID_ARGUMENT;
+    if (workspace_bytes < need) return CONV2D_ERR_WORKSPACE_TOO_SMALL;
+    const Fp4MatmulArgs a = {p->m, p->n, p->k, (int)ceil_div(p->k, kFp4Group), p->x_row, p->w_pitch, x, (const uint8_t *)w,
+                             (const uint8_t *)w_scale, out, plan.splits, plan.per, (float *)workspace};
     return status(launch_fp4_matmul(dtype, a, (hipStream_t)stream));
 }
 

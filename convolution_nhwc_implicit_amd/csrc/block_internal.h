@@ -110,7 +110,15 @@ struct Fp4MatmulArgs {
     const void *x;
     const uint8_t *w, *w_scale;
     void *out;
+    int splits, per;  // Fp4Plan
+    float *partial;   // [splits][m][n]
 };
+// Many rows of x: workgroups along k and the turns of 256 values of each.  splits 0: few.
+struct Fp4Plan {
+    int splits, per;
+    size_t bytes(int m, int n) const { return splits > 1 ? (size_t)splits * m * n * 4 : 0; }
+};
+Fp4Plan fp4_matmul_plan(int m, int n, int k, int dtype);
 hipError_t launch_fp4_quantize(int dtype, const Fp4QuantArgs &a, hipStream_t st);
 hipError_t launch_fp4_matmul(int dtype, const Fp4MatmulArgs &a, hipStream_t st);
 

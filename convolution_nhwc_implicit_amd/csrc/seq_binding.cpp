@@ -843,8 +843,10 @@ PyObject *py_fp4_matmul(PyObject *, PyObject *const *a, Py_ssize_t n)
     c.detached("fp4_matmul", "quantised weights have none");
     const fp4_matmul_problem_t p = {int_size(m, "m"), int_size(rows, "n"), int_size(k, "k"), row_stride(*x), pitch};
     const c10::DeviceGuard guard(x->device());
-    const Tensor out = new_tensor(*x, {m, rows}, x->scalar_type());
-    raise(fp4_matmul(&p, code, ptr(x), ptr(w), ptr(ws), out_ptr(out), stream_of(*x)), "fp4_matmul");
+    size_t need = 0;
+    raise(fp4_matmul_workspace_size(&p, code, &need), "fp4_matmul_workspace_size");
+    const Tensor out = new_tensor(*x, {m, rows}, x->scalar_type()), work = workspace(*x, need);
+    raise(fp4_matmul(&p, code, ptr(x), ptr(w), ptr(ws), out_ptr(out), out_ptr(work), need, stream_of(*x)), "fp4_matmul");
     return wrap(out);
     END_HANDLE_TH_ERRORS
 }

@@ -342,7 +342,8 @@ int layer_norm_grad(const layer_norm_problem_t *prob, int dtype, int param_dtype
 /*
  * 4-bit operands: e2m1 values (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives), two
  * to a byte with the even one in the low half, and for every 32 values of a row one
- * byte e that scales them by 2^(e - 127); e = 255 makes them NaN.
+ * byte e that scales them by 2^(e - 127); e = 255 makes them NaN.  Values past fp32's
+ * range (e of 253 and 254) count as infinite; in products with fp16 x, e = 0 may count as 0.
  *
  * fp4_quantize: x [m][k] (dtype, row stride x_row, in elements) to such an operand,
  * q [m][q_pitch] bytes and scale [m][ceil(k/32)].  The scale is the least power of
@@ -361,15 +362,17 @@ int fp4_quantize(int dtype, int m, int k, const void *x, long long x_row, void *
  *   x [m][k], row stride x_row; w [n][w_pitch] bytes, 16-byte aligned, w_pitch a
  *   multiple of 16, at least 16 * ceil(k/32); w_scale [n][ceil(k/32)]; out [m][n]
  *   dense; must not overlap the operands.
- * Halves of bytes past k are read but have no influence.
+ * Halves of bytes past k are read but have no influence.  The workspace (16-byte
+ * aligned; its size may be 0) holds partial sums over k.
  */
 typedef struct fp4_matmul_problem {
     int m, n, k;
     long long x_row, w_pitch;
 } fp4_matmul_problem_t;
 
+int fp4_matmul_workspace_size(const fp4_matmul_problem_t *prob, int dtype, size_t *bytes);
 int fp4_matmul(const fp4_matmul_problem_t *prob, int dtype, const void *x, const void *w,
-               const void *w_scale, void *out, void *stream);
+               const void *w_scale, void *out, void *workspace, size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

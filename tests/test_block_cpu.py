@@ -267,7 +267,7 @@ def test_fp4_abi():
     f = LIB.fp4_matmul
 
     def call(p, dtype=BF16C, **kw):
-        a = dict(x=AT, w=AT, s=AT, out=AT)
+        a = dict(x=AT, w=AT, s=AT, out=AT, work=AT, size=ct.c_size_t(1 << 40))
         a.update(kw)
         return f(ct.byref(p) if p else None, dtype, *a.values(), None)
 
@@ -279,6 +279,10 @@ def test_fp4_abi():
     assert call(p, I8C) == UNSUPPORTED and call(p, w=P(8 + (1 << 20))) == UNSUPPORTED
     for name in ("x", "w", "s", "out"):
         assert call(p, **{name: None}) == INVALID
+    p = Fp4(48, 1024, 8192, 8192, 4096)
+    status, need = size("fp4_matmul_workspace_size", p, BF16C)
+    assert status == OK and need > 0  # few columns: workgroups split k
+    assert call(p, size=ct.c_size_t(need - 1)) == SMALL and call(p, work=None) == INVALID and call(p, work=P(8 + (1 << 20))) == UNSUPPORTED
 
 
 # ----------------------------------------------------------------------- the plain forms that kernels are held to

@@ -482,7 +482,7 @@ def fp4_weights(g, n, k):
     return q, scale, R.fp4_values(q.cpu(), scale.cpu(), k)
 
 
-FP4 = [(1, 1, 1, F32), (1, 16, 32, BF16), (1, 300, 4096, BF16), (2, 17, 33, F16), (16, 100, 1000, BF16), (17, 64, 160, F32),
+FP4 = [(20, 130, 4096, BF16), (64, 300, 2050, F16), (40, 129, 1024, F16), (17, 128, 8200, BF16), (100, 257, 700, F16), (33, 1, 600, BF16), (1, 1, 1, F32), (1, 16, 32, BF16), (1, 300, 4096, BF16), (2, 17, 33, F16), (16, 100, 1000, BF16), (17, 64, 160, F32),
        (33, 257, 4104, F16), (48, 40, 777, BF16), (64, 130, 2048, F32), (65, 31, 511, BF16), (150, 96, 95, F16), (5, 1000, 31, F32)]
 
 
@@ -522,6 +522,27 @@ def test_fp4_matmul_scales():
     assert torch.equal(got[0, :255], want[:255]) and bool(got[:, 255].isnan().all())
     normal = want[:255] * 2.0 ** -20 >= 2.0 ** -126
     assert torch.equal(got[1, :255][normal], (want[:255] * 2.0 ** -20)[normal])
+
+
+@pytest.mark.parametrize("m", [2, 40])
+@pytest.mark.parametrize("typ", [F16, BF16], ids=str)
+def test_fp4_matmul_scales_in_16_bits(typ, m):
+    """Every scale byte next to every other (256 rows of two groups): fp16 weights hold only some of them."""
+    g = gen(24)
+    n, k = 256, 64
+    q = torch.randint(0, 256, (n, 32), generator=g).to(torch.uint8)
+    scale = torch.stack([torch.arange(n), torch.arange(n).roll(1)], 1).to(torch.uint8)
+    x = randn(g, m, k, dtype=typ)
+    x[1] *= 2.0 ** -14  # fp16's subnormal numbers among them
+    got = nn.fp4_matmul(x.to(DEV), q.to(DEV), scale.to(DEV)).double().cpu()
+    w = R.fp4_values(q, scale, k)
+    want, mag = x.double() @ w.t(), x.double().abs() @ w.abs().t()
+    top = torch.finfo(typ).max
+    # a sum's roundings, below fp32's normal numbers half its least step each; the result's half step, or its least
+    tol = 70 * R.U * mag + R.half_step(typ) * want.abs() + torch.finfo(typ).smallest_normal * torch.finfo(typ).eps + 70 * 2.0 ** -150
+    ok = ((got - want).abs() <= tol) | (want.isnan() & got.isnan()) | ((want.abs() >= top * 0.99) & (got.abs() >= top * 0.99))
+    # past fp32's range: between the terms of a sum, or the weights themselves (6 * 2^126 is 2^128.6)
+    assert (ok | (mag >= 2.0 ** 127) | (w.abs().amax(1) >= 2.0 ** 128)).all()
 
 
 @pytest.mark.parametrize("typ", [F16, BF16, F32], ids=str)
