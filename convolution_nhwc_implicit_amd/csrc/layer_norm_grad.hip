@@ -8,6 +8,10 @@
 // columns of the weight's and the bias's gradients; they leave as one partial sum for
 // each workgroup, and column_sums adds those.  Two sums over the lanes a row: the mean;
 // then the squares around it, g, and g times the distance from the mean together.
+//
+// Bound by memory: 16384 rows of 4096 bf16, with dtotal, 111 us (5.0 TB/s with the
+// partial sums) and 5 us for their sum.  The next row's loads ahead of the sums, and up
+// to six workgroups to a compute unit instead of two, changed nothing.
 #include "norm_common.h"
 
 namespace cnv {

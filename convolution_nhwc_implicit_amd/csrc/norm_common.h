@@ -11,6 +11,8 @@ __device__ inline float norm_dpp(float v)
     return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
 }
 
+__device__ inline float sum_of(uint32_t a, uint32_t b) { return __builtin_bit_cast(float, a) + __builtin_bit_cast(float, b); }
+
 // The sum of v over the LANES lanes (16 or 64) around this one, the same bits in all of them.
 template <int LANES>
 __device__ inline float lanes_sum(float v)
@@ -19,9 +21,13 @@ __device__ inline float lanes_sum(float v)
     v += norm_dpp<0x124>(v);
     v += norm_dpp<0x122>(v);
     v += norm_dpp<0x121>(v);
-    if (LANES > 16) {
-        v += __shfl_xor(v, 16);
-        v += __shfl_xor(v, 32);
+    if (LANES > 16) {  // rows change places with their neighbours, then the wave's halves
+        typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+        uint32_t u = __builtin_bit_cast(uint32_t, v);
+        u32x2 r = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(u, u, false, false));
+        u = __builtin_bit_cast(uint32_t, sum_of(r[0], r[1]));
+        r = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(u, u, false, false));
+        v = sum_of(r[0], r[1]);
     }
     return v;
 }
