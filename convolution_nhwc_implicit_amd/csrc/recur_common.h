@@ -16,10 +16,14 @@ struct RecurChannels {
     {
         load_vec<SF32, VC>(A_ + c, VC, A);
 #pragma unroll
+        for (int v = 0; v < VC; ++v) rb[v] = ib[v] = 0.0f;
+        if (r_bias) load_vec<SF32, VC>(r_bias + c, VC, rb);
+        if (i_bias) load_vec<SF32, VC>(i_bias + c, VC, ib);
+#pragma unroll
         for (int v = 0; v < VC; ++v) {
             A[v] = (A[v] < -2e38f ? -2e38f : A[v]) * kLog2e;
-            rb[v] = (r_bias ? r_bias[c + v] : 0.0f) * -kLog2e;
-            ib[v] = (i_bias ? i_bias[c + v] : 0.0f) * -kLog2e;
+            rb[v] *= -kLog2e;
+            ib[v] *= -kLog2e;
         }
     }
 };
