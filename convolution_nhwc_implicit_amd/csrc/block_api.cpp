@@ -39,8 +39,10 @@ bool one_stride(const seq_batch_t &b, const seq_stride_t &s) { return b.seq_star
 // chunks are read twice; else they are cut so that each unit has as many workgroups as
 // it holds: two in the forward pass, one in the gradient's.  (8192 tokens of 4096 bf16
 // channels: forward 132 us with two, 139 with one; 3 x 517 of 768, gradients: 48 us with
-// one, 58 with two.)  A row's 128 bytes to a workgroup: with 64 of them and twice the
-// workgroups the walks take 150 us, and the training step 730 instead of 530.
+// one, 58 with two.)  Whole sequences give a workgroup 128 bytes of a row (with 64 and
+// twice the workgroups the training step of 4 x 4096 x 4096 takes 730 us instead of 530),
+// cut ones, which can make up for it by shorter chunks, 256: the 8192 tokens' walk to
+// the outputs takes 63 us, 5.3 TB/s, with 128 it took 73.
 // Chunks run over all tokens, sequences' borders inside them, unless a dense batch's
 // sequences lie apart.
 RecurPlan recur_plan(const gated_recurrence_problem_t *p, int dtype, bool grad)
@@ -54,10 +56,12 @@ RecurPlan recur_plan(const gated_recurrence_problem_t *p, int dtype, bool grad)
     // sequences that are walked whole; all tokens together where their lengths are on the device
     const long long walks = b.seq_start ? 1 : b.seqs;
     while (r.shape.lanes > 8 && p->d <= r.shape.channels() / 2) r.shape.lanes /= 2;
+    const bool cut = ceil_div(p->d, r.shape.channels()) * walks < kCUs;
+    if (cut && p->d > r.shape.channels()) r.shape.lanes *= 2;
     const int segment = recur_segment(r.shape);
     const long long across = ceil_div(p->d, r.shape.channels());
     long long chunk = b.tokens;
-    if (across * walks < kCUs) chunk = ceil_div(b.tokens, ceil_div(grad ? kCUs : 2 * kCUs, across));
+    if (cut) chunk = ceil_div(b.tokens, ceil_div(grad ? kCUs : 2 * kCUs, across));
     else if (!b.seq_start && b.len >= segment) {
         chunk = b.len;
         if (b.len % segment) flat = false;

@@ -47,6 +47,7 @@ __global__ __launch_bounds__(64 * kRecurWaves, 4) void recur_kernel(RecurArgs a)
     if (ENDS && a.per_seq) index += index / (a.per_seq - 1);
     const Place at(id % a.across, a.d);
     RecurChunk chunk(a, bits, index);
+    const RecurStarts starts(a.q);
     const RecurChannels<VC> ch(a.A, a.r_bias, a.i_bias, at.c);
     const RecurRows<E, VC> xr(a.x, a.xs, a, chunk, at), rr(a.r, a.rs, a, chunk, at), ir(a.i, a.is, a, chunk, at), zr(a.z, a.zs, a, chunk, at);
     const RecurOut<E, VC> yr(a.y, a, chunk, at);
@@ -75,18 +76,12 @@ __global__ __launch_bounds__(64 * kRecurWaves, 4) void recur_kernel(RecurArgs a)
 #pragma unroll
     for (int j = 0; j < T; ++j) load(j, std::false_type{});
 
+    if (!ENDS && a.joined) recur_carry<VC, W>(a.chunk_decay, a.chunk_state, chunk.before, index, 1, a.d, at, ends[1]);
     chunk.mark(a);
     float carry[VC] = {};
     RecurPiece<VC> total;
     total.clear();
-    if (!ENDS && a.joined)
-#pragma unroll 4
-        for (int k = chunk.before; k < index; ++k) {
-            RecurPiece<VC> p;
-            recur_get<VC>(a.chunk_decay, k, a.d, at.c, p.dec);
-            recur_get<VC>(a.chunk_state, k, a.d, at.c, p.end);
-            p.template carry<false>(carry);
-        }
+    if (!ENDS && a.joined) recur_carried<VC, W>(ends[1], at, carry);  // the first segment uses ends[0]
 
     // INSIDE: this segment lies inside a sequence, and all of the next one's tokens are there
     auto segment = [&](int seg, auto inside) {
@@ -113,7 +108,7 @@ __global__ __launch_bounds__(64 * kRecurWaves, 4) void recur_kernel(RecurArgs a)
         if (!INSIDE) {
             recur_cut<VC, T>(run, bv);
             if (run.firsts && a.initial)  // what the initial states bring is an input of the first tokens
-                recur_gather<VC, T>(a, a.initial, run.f, t0, at.c, [&](int j, const float (&h)[VC]) {
+                recur_gather<VC, T>(a, starts, a.initial, run.f, t0, at, [&](int j, const float (&h)[VC]) {
 #pragma unroll
                     for (int v = 0; v < VC; ++v) bv[j][v] = fmaf(av[j][v], h[v], bv[j][v]);
                 });
@@ -140,7 +135,7 @@ __global__ __launch_bounds__(64 * kRecurWaves, 4) void recur_kernel(RecurArgs a)
             }
             yr.template store<INSIDE>(y, j, out);
         }
-        if (!INSIDE && run.lasts && a.final_state) recur_scatter<VC, T>(a, run.last, t0, at, av, a.final_state);
+        if (!INSIDE && run.lasts && a.final_state) recur_scatter<VC, T>(a, starts, run.last, t0, at, av, a.final_state);
     };
     for (int seg = 0, begin = 0; seg < chunk.len; seg += kSegment) {
         while (begin < seg) begin = chunk.next(seg, a.chunk);

@@ -43,6 +43,7 @@ __global__ __launch_bounds__(64 * kRecurWaves) void recur_states_kernel(RecurArg
     const int index = id / a.across;
     const Place at(id % a.across, a.d);
     RecurChunk chunk(a, bits, index);
+    const RecurStarts starts(a.q);
     const RecurChannels<VC> ch(a.A, a.r_bias, a.i_bias, at.c);
     const Tensors<E, VC> in(a, chunk, at);
     const bool gate = BACK && a.z;
@@ -111,7 +112,7 @@ __global__ __launch_bounds__(64 * kRecurWaves) void recur_states_kernel(RecurArg
         }
         const long long t0 = chunk.c0 + seg + lead + at.q * T;
         if (!INSIDE && run.firsts && a.initial)
-            recur_gather<VC, T>(a, a.initial, run.f, t0, at.c, [&](int j, const float (&h)[VC]) {
+            recur_gather<VC, T>(a, starts, a.initial, run.f, t0, at, [&](int j, const float (&h)[VC]) {
 #pragma unroll
                 for (int v = 0; v < VC; ++v) bv[j][v] = fmaf(av[j][v], h[v], bv[j][v]);
             });
@@ -121,7 +122,7 @@ __global__ __launch_bounds__(64 * kRecurWaves) void recur_states_kernel(RecurArg
         join.put(ends[buf][0]);
         if constexpr (BACK) {
             if (!INSIDE && run.lasts && a.dfinal)
-                recur_gather<VC, T>(a, a.dfinal, run.last, t0, at.c, [&](int j, const float (&k)[VC]) {
+                recur_gather<VC, T>(a, starts, a.dfinal, run.last, t0, at, [&](int j, const float (&k)[VC]) {
 #pragma unroll
                     for (int v = 0; v < VC; ++v) gv[j][v] += k[v];
                 });
@@ -180,6 +181,7 @@ __global__ __launch_bounds__(64 * kRecurWaves) void recur_grad_kernel(RecurArgs 
     const int index = id / a.across;
     const Place at(id % a.across, a.d);
     RecurChunk chunk(a, bits, index);
+    const RecurStarts starts(a.q);
     const RecurChannels<VC> ch(a.A, a.r_bias, a.i_bias, at.c);
     const Tensors<E, VC> in(a, chunk, at);
     const RecurOut<E, VC> dxr(a.dx, a, chunk, at), drr(a.dr, a, chunk, at), dir(a.di, a, chunk, at), dzr(a.dz, a, chunk, at);
@@ -211,24 +213,17 @@ __global__ __launch_bounds__(64 * kRecurWaves) void recur_grad_kernel(RecurArgs 
     aim(RecurSpan(chunk, at, (segs > 0 ? segs - 1 : 0) * kSegment + lead));
 #pragma unroll
     for (int j = 0; j < T; ++j) load(j, std::false_type{});
-    chunk.mark(a);
     float start[VC] = {}, flow[VC] = {};  // the state the chunk starts with; the gradient that flows in behind it
+    const int other = segs & 1;  // the last segment, which comes first, uses the other half of ends
     if (a.joined) {
         const int after = a.per_seq ? chunk.before + a.per_seq : a.chunks;
-#pragma unroll 4
-        for (int k = chunk.before; k < index; ++k) {
-            RecurPiece<VC> p;
-            recur_get<VC>(a.chunk_decay, k, a.d, at.c, p.dec);
-            recur_get<VC>(a.chunk_state, k, a.d, at.c, p.end);
-            p.template carry<false>(start);
-        }
-#pragma unroll 4
-        for (int k = after - 1; k > index; --k) {
-            RecurPiece<VC> p;
-            recur_get<VC>(a.back_decay, k, a.d, at.c, p.dec);
-            recur_get<VC>(a.chunk_back, k, a.d, at.c, p.end);
-            p.template carry<false>(flow);
-        }
+        recur_carry<VC, W>(a.chunk_decay, a.chunk_state, chunk.before, index, 1, a.d, at, ends[other][0]);
+        recur_carry<VC, W>(a.back_decay, a.chunk_back, after - 1, index, -1, a.d, at, ends[other][1]);
+    }
+    chunk.mark(a);
+    if (a.joined) {
+        recur_carried<VC, W>(ends[other][0], at, start);
+        recur_carried<VC, W>(ends[other][1], at, flow);
     }
     // INSIDE: this segment lies inside a sequence, and another one is before it
     auto segment = [&](int seg, auto inside) {
@@ -265,12 +260,12 @@ __global__ __launch_bounds__(64 * kRecurWaves) void recur_grad_kernel(RecurArgs 
             recur_cut<VC, T>(run, gv);
         }
         if (!INSIDE && run.firsts && a.initial)
-            recur_gather<VC, T>(a, a.initial, run.f, t0, at.c, [&](int j, const float (&h)[VC]) {
+            recur_gather<VC, T>(a, starts, a.initial, run.f, t0, at, [&](int j, const float (&h)[VC]) {
 #pragma unroll
                 for (int v = 0; v < VC; ++v) hv[j][v] = fmaf(av[j][v], h[v], hv[j][v]);
             });
         if (!INSIDE && run.lasts && a.dfinal)
-            recur_gather<VC, T>(a, a.dfinal, run.last, t0, at.c, [&](int j, const float (&k)[VC]) {
+            recur_gather<VC, T>(a, starts, a.dfinal, run.last, t0, at, [&](int j, const float (&k)[VC]) {
 #pragma unroll
                 for (int v = 0; v < VC; ++v) gv[j][v] += k[v];
             });
@@ -298,7 +293,7 @@ __global__ __launch_bounds__(64 * kRecurWaves) void recur_grad_kernel(RecurArgs 
                 h[v] = fmaf(av[j][v], h[v], b);
             }
         if (!INSIDE && run.firsts && a.initial)
-            recur_gather<VC, T>(a, a.initial, run.f, t0, at.c, [&](int j, const float (&h0)[VC]) {
+            recur_gather<VC, T>(a, starts, a.initial, run.f, t0, at, [&](int j, const float (&h0)[VC]) {
 #pragma unroll
                 for (int v = 0; v < VC; ++v) hv[j][v] = h0[v];
             });
@@ -331,7 +326,7 @@ __global__ __launch_bounds__(64 * kRecurWaves) void recur_grad_kernel(RecurArgs 
             dzr.template store<INSIDE>(dz, j, oz);
             __builtin_amdgcn_sched_barrier(0);  // a token's roots, worked out for all of them at once, would spill
         }
-        if (!INSIDE && run.firsts && a.dinitial) recur_scatter<VC, T>(a, run.f, t0, at, gv, a.dinitial);
+        if (!INSIDE && run.firsts && a.dinitial) recur_scatter<VC, T>(a, starts, run.f, t0, at, gv, a.dinitial);
     };
     for (int sg = segs - 1; sg >= 0; --sg) {
         // whether a sequence begins in it or right behind it, or tokens are missing

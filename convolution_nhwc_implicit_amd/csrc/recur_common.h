@@ -406,6 +406,45 @@ __device__ inline void recur_cut(const RecurRun<T> &run, float (&in)[T][VC])
             for (int v = 0; v < VC; ++v) in[j][v] = j < run.n ? in[j][v] : 0.0f;
 }
 
+// The chunks from `first` up (or down, by `step`) to the one before `stop` as one piece
+// each for the workgroup's waves, successive ones to a wave, so that their loads are all
+// under way together; into lds, for recur_carried() behind a barrier.
+template <int VC, int W, class Place, class Lds>
+__device__ inline void recur_carry(const float *decay, const float *end, int first, int stop, int step, int d, const Place &at, Lds &lds)
+{
+    const int all = (stop - first) * step, per = (all + W - 1) / W;
+    int left = all - at.wave * per;
+    left = left < per ? left : per;
+    RecurPiece<VC> mine;
+    mine.clear();
+    for (int k = first + at.wave * per * step; left > 0; left -= 4, k += 4 * step) {
+        RecurPiece<VC> p[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const long long chunk = k + (i < left ? i : left - 1) * step;
+            recur_get<VC>(decay, chunk, d, at.c, p[i].dec);
+            recur_get<VC>(end, chunk, d, at.c, p[i].end);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < left) {
+                p[i].template after<false>(mine);
+                mine = p[i];
+            }
+    }
+    if (at.q == 0) mine.put(&lds[at.wave][at.slot]);
+}
+template <int VC, int W, class Place, class Lds>
+__device__ inline void recur_carried(const Lds &lds, const Place &at, float (&h)[VC])
+{
+#pragma unroll 4
+    for (int w = 0; w < W; ++w) {
+        RecurPiece<VC> p;
+        p.get(&lds[w][at.slot]);
+        p.template carry<false>(h);
+    }
+}
+
 // What a run does to a state, from its decays and inputs.
 template <int VC, int T>
 __device__ inline void recur_piece(uint32_t f, bool firsts, const float (&av)[T][VC], const float (&bv)[T][VC], RecurPiece<VC> &p)
@@ -457,43 +496,61 @@ __device__ inline void recur_flow(uint32_t last, bool lasts, const float (&av)[T
     }
 }
 
-// The sequences of a run's tokens, in order.
-struct RecurSeqs {
-    const Seqs &q;
-    int s;
-    __device__ inline RecurSeqs(const Seqs &q_, long long t0) : q(q_), s(q_.find(t0)) {}
-    __device__ inline int at(long long t)
+// Where sequences begin, a lane each, if there are that few: finding a token's sequence
+// then waits for no memory, where a search waits for a load each time it halves.
+struct RecurStarts {
+    int v;
+    bool few;
+    __device__ inline RecurStarts(const Seqs &q) : v(0), few(q.start && q.seqs <= 64)
     {
-        while (s + 1 < q.seqs && q.begin(s + 1) <= t) ++s;
-        return s;
+        const int lane = threadIdx.x % 64;
+        if (few) v = lane < q.seqs ? (int)q.begin(lane) : INT32_MAX;
+    }
+    // The sequence of row t, whole waves at a time; t differs between a wave's groups of lanes.
+    template <class Place>
+    __device__ inline int find(const Seqs &q, const Place &at, long long t) const
+    {
+        if (!few) return q.find(t);
+        int s = 0;
+#pragma unroll
+        for (int g = 0; g < Place::Q; ++g) {
+            const int tg = __builtin_amdgcn_readlane((int)t, g * (64 / Place::Q));
+            const int n = __builtin_popcountll(__ballot(v <= tg)) - 1;
+            s = at.q == g ? n : s;
+        }
+        return s < 0 ? 0 : s;
     }
 };
 
 // Entries of p [seqs][d] for the tokens in `which` (from row t0 on): each goes to
 // use(j, the entry).
-template <int VC, int T, class F>
-__device__ inline void recur_gather(const RecurArgs &a, const float *p, uint32_t which, long long t0, int c, F use)
+template <int VC, int T, class Place, class F>
+__device__ inline void recur_gather(const RecurArgs &a, const RecurStarts &starts, const float *p, uint32_t which, long long t0,
+                                    const Place &at, F use)
 {
-    if (which == 0) return;
-    RecurSeqs seq(a.q, t0);
 #pragma unroll
     for (int j = 0; j < T; ++j)
-        if (which >> j & 1) {
-            float h[VC];
-            recur_get<VC>(p, seq.at(t0 + j), a.d, c, h);
-            use(j, h);
+        if (__ballot(which >> j & 1)) {
+            const int s = starts.find(a.q, at, t0 + j);
+            if (which >> j & 1) {
+                float h[VC];
+                recur_get<VC>(p, s, a.d, at.c, h);
+                use(j, h);
+            }
         }
 }
 
 // Writes the values of tokens in `which` to their sequences' entries of out [seqs][d].
 template <int VC, int T, class Place>
-__device__ inline void recur_scatter(const RecurArgs &a, uint32_t which, long long t0, const Place &at, const float (&hv)[T][VC], float *out)
+__device__ inline void recur_scatter(const RecurArgs &a, const RecurStarts &starts, uint32_t which, long long t0, const Place &at,
+                                     const float (&hv)[T][VC], float *out)
 {
-    if (which == 0 || !at.mine) return;
-    RecurSeqs seq(a.q, t0);
 #pragma unroll
     for (int j = 0; j < T; ++j)
-        if (which >> j & 1) recur_put<VC>(out, seq.at(t0 + j), a.d, at.c, hv[j]);
+        if (__ballot(which >> j & 1)) {
+            const int s = starts.find(a.q, at, t0 + j);
+            if ((which >> j & 1) && at.mine) recur_put<VC>(out, s, a.d, at.c, hv[j]);
+        }
 }
 
 // Blocks that read the same lines of memory (neighbouring channels of one chunk) go to
@@ -511,7 +568,8 @@ hipError_t recur_by_shape(const RecurShape &s, F f)
     switch (s.lanes) {
         case 8: return f(vc, integral_constant<int, 8>{});
         case 16: return f(vc, integral_constant<int, 16>{});
-        default: return f(vc, integral_constant<int, 32>{});
+        case 32: return f(vc, integral_constant<int, 32>{});
+        default: return f(vc, integral_constant<int, 64>{});
     }
 }
 
