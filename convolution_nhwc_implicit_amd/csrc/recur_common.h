@@ -8,7 +8,8 @@
 namespace cnv {
 
 // A lane's channels' parameters, scaled for exponentials to the base 2: A times log2 e
-// (clamped so that its product with a closed gate is 0), the biases times -log2 e.
+// (clamped so that its product with a closed gate is 0; below the normal numbers, whose
+// inverse the gradients take, 0), the biases times -log2 e.
 template <int VC>
 struct RecurChannels {
     float A[VC], rb[VC], ib[VC];
@@ -21,6 +22,7 @@ struct RecurChannels {
         if (i_bias) load_vec<SF32, VC>(i_bias + c, VC, ib);
 #pragma unroll
         for (int v = 0; v < VC; ++v) {
+            if (fabsf(A[v]) < 0x1p-126f) A[v] = 0.0f;
             A[v] = (A[v] < -2e38f ? -2e38f : A[v]) * kLog2e;
             rb[v] *= -kLog2e;
             ib[v] *= -kLog2e;

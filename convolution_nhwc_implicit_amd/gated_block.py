@@ -205,7 +205,8 @@ class RecurrentBlock:
 
     def train(self, u, dout, seq_start=None, residual=None):
         """Outputs for u (and residual) [tokens][model] and, for (gradient of out, gradient of total or None) =
-        dout(out, total), the gradients of u (the residual's too) and of every weight: (out, total, dict)."""
+        dout(out, total), the gradients of u (the residual's too) and of every weight: (out, total, dict). The sequences
+        have to cover all of u's rows."""
         h, total = self._norm(u, residual)
         x0, z = self.in_proj(h).split(self.d, -1)
         conv = dict(silu=True, seq_start=seq_start)

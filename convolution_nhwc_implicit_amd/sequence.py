@@ -112,7 +112,7 @@ def gated_recurrence(x, r, i, A, z=None, r_bias=None, i_bias=None, initial_state
     token after token and channel by channel.
 
     x, r, i, z [..][d] in one type; A (log decays, at most 0), r_bias, i_bias [d] and the states [seqs][d] in float32.
-    Positive A gives NaN; rates below -2e38 count as -2e38. With return_state the result is (y, final_state)."""
+    Positive A gives NaN; rates below -2e38 count as -2e38, those nearer to 0 than 2^-126 as 0. With return_state the result is (y, final_state)."""
     return load().gated_recurrence(x, r, i, A, z, r_bias, i_bias, initial_state, seq_start, return_state)
 
 

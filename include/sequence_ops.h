@@ -254,7 +254,8 @@ int fp8_matmul(const fp8_matmul_problem_t *prob, int dtype, const void *a, const
  *             not overlap.
  *   y [tokens][d] dense, dtype; must not overlap the inputs
  * Decays are also multiplied over runs of tokens before they meet a state: an
- * infinite state is NaN where such a product is 0.  Gates below 2^-126 count as 0.
+ * infinite state is NaN where such a product is 0.  Gates and rates below 2^-126
+ * count as 0.
  * Row strides and d are below 2^24.  Long sequences are cut into chunks that run
  * side by side, joined through the workspace (16-byte aligned; its size may be 0).
  */
@@ -362,8 +363,9 @@ int fp4_quantize(int dtype, int m, int k, const void *x, long long x_row, void *
  *   x [m][k], row stride x_row; w [n][w_pitch] bytes, 16-byte aligned, w_pitch a
  *   multiple of 16, at least 16 * ceil(k/32); w_scale [n][ceil(k/32)]; out [m][n]
  *   dense; must not overlap the operands.
- * Halves of bytes past k are read but have no influence.  The workspace (16-byte
- * aligned; its size may be 0) holds partial sums over k.
+ * Halves of bytes past k are read but have no influence (under infinite scales they
+ * have to be zero).  The workspace (16-byte aligned; its size may be 0) holds partial
+ * sums over k.
  */
 typedef struct fp4_matmul_problem {
     int m, n, k;

@@ -63,6 +63,11 @@ RECUR = [
     ([1500], False, 64, F32, False, False, True),
     ([700, 900], True, 64, F16, True, True, True),
     ([0, 0], True, 5, F32, True, True, True),
+    ([4, 0, 3], True, 1, BF16, True, True, True),
+    (list(range(64)), True, 258, BF16, True, True, True),
+    (list(range(65)), True, 100, F32, True, False, True),
+    ([3, 7000, 2, 1500, 1], True, 7, F32, True, True, True),
+    ([2500], False, 300, F16, True, True, True),
 ]
 
 
@@ -306,6 +311,44 @@ def test_recurrence_long_sequences_that_lie_apart():
         assert same_but_for_chunks(k["dinitial_state"][s], k1["dinitial_state"][0])
         # gradients of gates add terms of some tens
         assert all(float((k[n][s] - k1[n]).abs().max()) <= 1e-4 for n in ("dx", "dr", "di", "dz"))
+
+
+def test_recurrence_least_rates():
+    """Rates whose inverses pass float32's range: below 2^-126 they count as 0."""
+    A = -torch.tensor([1e-45, 1e-40, 1.1754942e-38, 1.1754944e-38, 3e-38, 1e-36])
+    g = gen(15)
+    c = [randn(g, 300, 6).to(DEV) for _ in range(4)]
+    dA = A.to(DEV)
+    y = nn.gated_recurrence(*c[:3], dA, z=c[3])
+    k = nn.gated_recurrence_grad(c[0], *c[:3], dA, z=c[3])
+    assert bool(y.isfinite().all()) and all(bool(k[n].isfinite().all()) for n in ("dx", "dr", "di", "dz", "dA"))
+    assert not y[:, :3].any() and not any(k[n][:, :3].any() for n in ("dx", "dr", "di", "dz")) and not k["dA"][:3].any()
+    h, lost = torch.zeros(3, dtype=torch.float64), torch.zeros(3, dtype=torch.float64)
+    x, r, i, z = (v[:, 3:].double().cpu() for v in c)
+    for t in range(300):
+        L = A[3:].double() * torch.sigmoid(r[t])
+        b = torch.sqrt(-torch.expm1(2 * L)) * torch.sigmoid(i[t]) * x[t]
+        h = torch.exp(L) * h + b
+        # log2 e L may count as 0 below 2^-126: a root of at most (2 ln 2)^0.5 2^-63; else 64 roundings of a term and
+        # one of the sum so far, at most 300 of them
+        lost += 2.0 ** -62 * x[t].abs() + (64 + 300) * R.U * b.abs()
+        silu = z[t] * torch.sigmoid(z[t])
+        assert bool(((y[t, 3:].double().cpu() - h * silu).abs() <= lost * silu.abs() + 64 * R.U * (h * silu).abs()).all())
+
+
+def test_recurrence_starts_out_of_order():
+    """Starts that descend or lie outside give unspecified results, and nothing else."""
+    case = ([40, 50, 60, 70], True, 66, BF16, True, True, True)
+    c, p, _, start = recur_case(case)
+    y, k = recur_call(p, start), recur_grads(p, start)
+    for bad in ([0, 90, 40, 150, 220], [220, 150, 90, 40, 0], [-7, 40, 1 << 30, 150, 220], [5, 5, 5, 5, 5], [-(1 << 31), 0, 0, 0, (1 << 31) - 1]):
+        t = torch.tensor(bad, dtype=torch.int32, device=DEV)
+        recur_call(p, t, state=True)
+        recur_grads(p, t)
+        torch.cuda.synchronize()
+    assert torch.equal(recur_call(p, start), y)
+    again = recur_grads(p, start)
+    assert all(torch.equal(again[n], k[n]) for n in k)
 
 
 # ------------------------------------------------------------------------------------------ layer norm
@@ -617,3 +660,43 @@ def test_streams_and_graphs(graph):
         assert all(torch.equal(a, b) for a, b in zip(got, want))
         together(p, start, nrm, q, scale, begin.clone())  # eager work between
         torch.cuda.synchronize()
+
+
+def test_two_streams_at_once():
+    """Calls that run side by side share nothing."""
+    cases = [([3000], False, 64, BF16, True, True, True), ([900, 0, 1300], True, 200, BF16, True, True, True)]
+    args = []
+    for case in cases:
+        c, p, _, start = recur_case(case)
+        d = case[2]
+        g = gen(33)
+        nrm = (1 + randn(g, d, scale=0.1, dtype=BF16)).to(DEV), randn(g, d, dtype=BF16).to(DEV)
+        flat = {k: v.reshape(-1, d) if k in ("x", "r", "i", "z", "dy") else v for k, v in p.items()}
+        args.append((flat, start if start is not None else torch.tensor([0, 3000], dtype=torch.int32, device=DEV), nrm,
+                     *fp4_weights(g, 300, d)[:2], randn(g, 5, d).to(DEV)))
+    run = lambda a: together(*a[:-1], a[-1].clone())
+    want = [run(a) for a in args]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in args]
+    got = []
+    for _ in range(10):
+        for a, s in zip(args, streams):
+            with torch.cuda.stream(s):
+                got.append(run(a))
+    torch.cuda.synchronize()
+    for k, g in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(g, want[k % 2]))
+
+
+def test_fp4_one_row_for_all():
+    """x with one row for all, and in a matrix with a row to spare."""
+    g = gen(35)
+    q, scale, _ = fp4_weights(g, 70, 200)
+    x = randn(g, 1, 200, dtype=F16).to(DEV)
+    want = nn.fp4_matmul(x, q, scale)
+    for m in (3, 40, 70):
+        got = nn.fp4_matmul(x.expand(m, 200), q, scale)
+        assert torch.equal(got, got[:1].expand(m, 70))
+        # sums of another order: both within 200 roundings of the sum of sizes
+        size = x.float().abs().max() * 200 * 6 * 2.0 ** (int(scale.max()) - 127)
+        assert bool(((got[0].double() - want[0].double()).abs() <= torch.finfo(F16).eps * want[0].double().abs() + 2.0 ** -24 + 400 * R.U * float(size)).all())
