@@ -3,6 +3,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cmath>
+#include <numeric>
 
 #include "block_internal.h"
 #include "seq_checks.h"
@@ -61,11 +62,13 @@ RecurPlan recur_plan(const gated_recurrence_problem_t *p, int dtype, bool grad)
     const int segment = recur_segment(r.shape);
     const long long across = ceil_div(p->d, r.shape.channels());
     long long chunk = b.tokens;
-    if (cut) chunk = ceil_div(b.tokens, ceil_div(grad ? kCUs : 2 * kCUs, across));
-    else if (!b.seq_start && b.len >= segment) {
-        chunk = b.len;
-        if (b.len % segment) flat = false;
-    }
+    if (!cut && !b.seq_start && b.len >= segment && b.len % segment) flat = false;
+    // sequences that whole segments hold, a few together where they are short
+    const long long whole = b.seq_start || b.len < 1 ? 0 : std::lcm((long long)b.len, (long long)segment);
+    if (!cut && !flat) chunk = b.len;
+    else if (!cut && whole > 0 && whole <= kRecurChunkMost && across * ceil_div(b.tokens, whole) >= kCUs)
+        chunk = whole * std::max(1LL, 256 / whole);
+    else if (cut || !b.seq_start) chunk = ceil_div(b.tokens, ceil_div(grad ? kCUs : 2 * kCUs, across));
     chunk = std::min(std::max(1LL, ceil_div(std::min(chunk, flat ? b.tokens : b.len), segment)) * segment, (long long)kRecurChunkMost);
     r.across = (int)across;
     r.chunk = (int)chunk;
@@ -398,7 +401,7 @@ int fp4_matmul(const fp4_matmul_problem_t *p, int dtype, const void *x, const vo
     if (need && !workspace) return CONV2D_ERR_INVALID_ARGUMENT;
     if (workspace_bytes < need) return CONV2D_ERR_WORKSPACE_TOO_SMALL;
     const Fp4MatmulArgs a = {p->m, p->n, p->k, (int)ceil_div(p->k, kFp4Group), p->x_row, p->w_pitch, x, (const uint8_t *)w,
-                             (const uint8_t *)w_scale, out, plan.splits, plan.per, (float *)workspace};
+                             (const uint8_t *)w_scale, out, plan.splits, plan.per, plan.tiles, (float *)workspace};
     return status(launch_fp4_matmul(dtype, a, (hipStream_t)stream));
 }
 

@@ -110,12 +110,13 @@ struct Fp4MatmulArgs {
     const void *x;
     const uint8_t *w, *w_scale;
     void *out;
-    int splits, per;  // Fp4Plan
+    int splits, per, tiles;  // Fp4Plan
     float *partial;   // [splits][m][n]
 };
-// Many rows of x: workgroups along k and the turns of 256 values of each.  splits 0: few.
+// Many rows of x: workgroups along k and the turns of 256 values of each.  splits 0: few
+// rows, and workgroups of one or two tiles of 16 rows of w (two for more than 16 rows of x).
 struct Fp4Plan {
-    int splits, per;
+    int splits, per, tiles;
     size_t bytes(int m, int n) const { return splits > 1 ? (size_t)splits * m * n * 4 : 0; }
 };
 Fp4Plan fp4_matmul_plan(int m, int n, int k, int dtype);

@@ -163,7 +163,6 @@ struct Eight {
     }
 };
 
-constexpr int kFew = 4;  // rows of x up to which 16 rows of w a workgroup are better than 32
 constexpr int kWaves = 8, kStep = 4;  // groups that the four lanes of a row load together
 // Steps whose weights are under way together.
 constexpr int steps_ahead(int mt, int nt) { return mt * nt == 1 ? 4 : 2; }
@@ -561,7 +560,7 @@ hipError_t launch_product(const Fp4MatmulArgs &a, hipStream_t st)
         constexpr int MT = decltype(mt)::value, NT = decltype(nt)::value;
         fp4_matmul_kernel<E, MT, NT><<<dim3((unsigned)((a.n + 16 * NT - 1) / (16 * NT)), (unsigned)((tiles + MT - 1) / MT)), 64 * kWaves, 0, st>>>(a);
     };
-    if (a.m <= kFew) go(integral_constant<int, 1>{}, integral_constant<int, 1>{});
+    if (a.tiles == 1 && tiles == 1) go(integral_constant<int, 1>{}, integral_constant<int, 1>{});
     else if (tiles == 1) go(integral_constant<int, 1>{}, integral_constant<int, 2>{});
     else if (tiles == 2) go(integral_constant<int, 2>{}, integral_constant<int, 2>{});
     else if (tiles == 3) go(integral_constant<int, 3>{}, integral_constant<int, 2>{});
@@ -571,14 +570,20 @@ hipError_t launch_product(const Fp4MatmulArgs &a, hipStream_t st)
 
 }  // namespace
 
-// Up to 16 rows of x workgroups read it whole and nothing has to be added up behind them:
-// 16 x 8192 x 4096 takes 10 us so and 13 with k split, 32 rows 14.5 and 13.8, 64 x 8192 x
-// 8192 41 and 23.  k is split until every compute unit has a workgroup (with two, 17 instead of
+// Few rows of x: workgroups of all of k for 32 rows of w, or 16 where that would leave
+// compute units without one (4 x 4096 x 4096 takes 5.8 us so and 7.5 with 32, 4 x 8192 x
+// 4096 10.1 and 8.3).  They read x whole each, at some 45 bytes a nanosecond for every
+// compute unit, which is what grows with the rows; past 4 us of that, 90000 values of x,
+// for the workgroups that follow each other on one, k is split, which costs as much
+// (16 x 8192 x 4096: 10.4 us, split 12.7; 48 rows 18.9 and 17.5; 4 x 32768 x 8192 45.7 and
+// 40.4, 16 rows 64 and 42; 4 x 4096 x 14336 14.7 and 15.5, 16 rows 22 and 16).  It is split until every compute unit has a workgroup (with two, 17 instead of
 // 14 us for 32 x 8192 x 4096), but into no less than two turns each.
 Fp4Plan fp4_matmul_plan(int m, int n, int k, int dtype)
 {
-    Fp4Plan p = {0, 0};
-    if (dtype == CONV2D_DTYPE_F32 || m <= 16) return p;
+    Fp4Plan p = {0, 0, ((long long)n + 31) / 32 < 256 ? 1 : 2};
+    const int wide = m <= 16 ? 16 * p.tiles : 32, rows = std::min(m, 64);
+    const long long rounds = ((((long long)n + wide - 1) / wide) * ((m + 63) / 64) + 255) / 256;
+    if (dtype == CONV2D_DTYPE_F32 || rounds * rows * k < 90000) return p;
     const long long blocks = ((long long)n + kManyRows - 1) / kManyRows * ((m + 63) / 64);
     const int whole = k / kTurn, splits = (int)std::max(1LL, std::min(256 / blocks, (long long)whole / 2));
     p.per = std::max(1, (whole + splits - 1) / splits);

@@ -68,6 +68,9 @@ RECUR = [
     (list(range(65)), True, 100, F32, True, False, True),
     ([3, 7000, 2, 1500, 1], True, 7, F32, True, True, True),
     ([2500], False, 300, F16, True, True, True),
+    ([16] * 300, False, 300, BF16, True, True, True),
+    ([5] * 300, False, 40, F32, True, True, True),
+    ([64] * 70, False, 256, F16, True, True, False),
 ]
 
 
@@ -525,7 +528,7 @@ def fp4_weights(g, n, k):
     return q, scale, R.fp4_values(q.cpu(), scale.cpu(), k)
 
 
-FP4 = [(20, 130, 4096, BF16), (64, 300, 2050, F16), (40, 129, 1024, F16), (17, 128, 8200, BF16), (100, 257, 700, F16), (33, 1, 600, BF16), (1, 1, 1, F32), (1, 16, 32, BF16), (1, 300, 4096, BF16), (2, 17, 33, F16), (16, 100, 1000, BF16), (17, 64, 160, F32),
+FP4 = [(4, 300, 30000, BF16), (16, 70, 7000, F16), (6, 8200, 8200, BF16), (20, 130, 4096, BF16), (64, 300, 2050, F16), (40, 129, 1024, F16), (17, 128, 8200, BF16), (100, 257, 700, F16), (33, 1, 600, BF16), (1, 1, 1, F32), (1, 16, 32, BF16), (1, 300, 4096, BF16), (2, 17, 33, F16), (16, 100, 1000, BF16), (17, 64, 160, F32),
        (33, 257, 4104, F16), (48, 40, 777, BF16), (64, 130, 2048, F32), (65, 31, 511, BF16), (150, 96, 95, F16), (5, 1000, 31, F32)]
 
 
