@@ -143,15 +143,17 @@ struct NormGradPlan {
     int per, parts;
     size_t partial, stats;
 };
-// Parts of rows, each with a partial sum of both parameters' gradients: as many as
-// give every compute unit a few workgroups, and no more, for they are written and read.
+// Parts of rows, each with a partial sum of both parameters' gradients, which is written
+// and read: as many as a compute unit holds workgroups.  Of 1024 lanes one (8192 rows of
+// 8192: 135 us, with two 146), of 256 and less four where a lane has one vector (16384 of
+// 2048: 56 us, with two 72), else two (16384 of 4096: 122 us, with four 131).
 NormGradPlan norm_grad_plan(const layer_norm_problem_t *p, int dtype)
 {
     NormGradPlan r;
     r.shape = layer_norm_grad_shape(dtype, p->d);
     const long long rows = (long long)p->seqs * p->len;
     const int groups = r.shape.held ? std::max(1, 256 / r.shape.lanes) : 1;
-    r.per = (int)(ceil_div(ceil_div(std::max(rows, 1LL), 2 * kCUs), groups) * groups);
+    r.per = (int)(ceil_div(ceil_div(std::max(rows, 1LL), (r.shape.lanes > 256 ? 1 : r.shape.vecs == 1 ? 4 : 2) * kCUs), groups) * groups);
     r.parts = (int)ceil_div(rows, r.per);
     r.partial = up((size_t)r.parts * 2 * p->d * 4);
     r.stats = r.shape.held ? 0 : up((size_t)rows * 16);

@@ -10,12 +10,28 @@
 // then the squares around it, g, and g times the distance from the mean together.
 //
 // Bound by memory: 16384 rows of 4096 bf16, with dtotal, 111 us (5.0 TB/s with the
-// partial sums) and 5 us for their sum.  The next row's loads ahead of the sums, and up
-// to six workgroups to a compute unit instead of two, changed nothing.
+// partial sums) and 5 us for their sum.  The next row's loads ahead of the sums changed
+// nothing; rows of two vectors a lane that are turned to fp32 at once spill with 1024
+// lanes (4096 of 16384: 302 us with their sum, as they are 182).
 #include "norm_common.h"
 
 namespace cnv {
 namespace {
+
+// Keeps 16-bit values as they lie in memory past here: as fp32, which the compiler would
+// keep them in rather than turn them again, rows of two vectors a lane take too many registers.
+template <class Raw, int N>
+__device__ inline void stay(Raw (&v)[N])
+{
+    if constexpr (N > 1 && sizeof(v[0].v[0]) == 2) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            u32x4 q = __builtin_bit_cast(u32x4, v[j]);
+            asm volatile("" : "+v"(q));
+            v[j] = __builtin_bit_cast(Raw, q);
+        }
+    }
+}
 
 template <class E, int LANES, int N, int V>
 __global__ __launch_bounds__(LANES > 256 ? LANES : 256) void norm_grad_kernel(NormArgs a)
@@ -33,51 +49,55 @@ __global__ __launch_bounds__(LANES > 256 ? LANES : 256) void norm_grad_kernel(No
     const long long first = (long long)blockIdx.x * a.per, last = first + a.per < a.rows ? first + a.per : a.rows;
     for (long long row = first + threadIdx.x / LANES; row < last; row += GROUPS) {
         const S *x = (const S *)a.x + a.at(a.xs, (int)row), *dy = (const S *)a.dy + a.at(a.dys, (int)row);
-        float t[N][V], g[N][V], extra[N][V];
+        typedef SVec<S, V> Raw;
+        Raw xv[N], gv[N], ev[N];
 #pragma unroll
-        for (int j = 0; j < N; ++j) load_vec<E, V>(x + at.col[j], V, t[j]);
+        for (int j = 0; j < N; ++j) xv[j] = *(const Raw *)(x + at.col[j]);
 #pragma unroll
-        for (int j = 0; j < N; ++j) load_vec<E, V>(dy + at.col[j], V, g[j]);
+        for (int j = 0; j < N; ++j) gv[j] = *(const Raw *)(dy + at.col[j]);
         if (a.dtotal) {
             const S *dt = (const S *)a.dtotal + a.at(a.dts, (int)row);
 #pragma unroll
-            for (int j = 0; j < N; ++j) load_vec<E, V>(dt + at.col[j], V, extra[j]);
+            for (int j = 0; j < N; ++j) ev[j] = *(const Raw *)(dt + at.col[j]);
         } else {
 #pragma unroll
             for (int j = 0; j < N; ++j)
 #pragma unroll
-                for (int i = 0; i < V; ++i) extra[j][i] = 0.0f;
+                for (int i = 0; i < V; ++i) ev[j].v[i] = (S)0;
         }
         float s1[1] = {0.0f};
 #pragma unroll
         for (int j = 0; j < N; ++j)
 #pragma unroll
-            for (int i = 0; i < V; ++i) s1[0] += at.mine(j, i) ? t[j][i] : 0.0f;
+            for (int i = 0; i < V; ++i) s1[0] += at.mine(j, i) ? E::to(xv[j].v[i]) : 0.0f;
         row_sum<LANES>(s1, slot[0]);
         const float mean = s1[0] / a.count;
+        stay(xv);
         float s[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int j = 0; j < N; ++j)
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                t[j][i] -= mean;
-                const float gw = g[j][i] * w[j][i];
-                s[0] += at.mine(j, i) ? t[j][i] * t[j][i] : 0.0f;
+                const float t = E::to(xv[j].v[i]) - mean, gw = E::to(gv[j].v[i]) * w[j][i];
+                s[0] += at.mine(j, i) ? t * t : 0.0f;
                 s[1] += at.mine(j, i) ? gw : 0.0f;
-                s[2] += at.mine(j, i) ? gw * t[j][i] : 0.0f;
+                s[2] += at.mine(j, i) ? gw * t : 0.0f;
             }
         row_sum<LANES>(s, slot[1]);
         const float rstd = 1.0f / sqrtf(s[0] / a.count + a.eps);
         const float c1 = s[1] / a.count, c2 = s[2] / a.count * rstd * rstd;
+        stay(xv);
+        stay(gv);
         S *dx = (S *)a.dx + row * a.d;
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             float o[V];
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                o[i] = rstd * (g[j][i] * w[j][i] - c1 - t[j][i] * c2) + extra[j][i];
-                dw[j][i] += g[j][i] * (t[j][i] * rstd);
-                db[j][i] += g[j][i];
+                const float t = E::to(xv[j].v[i]) - mean, g = E::to(gv[j].v[i]);
+                o[i] = rstd * (g * w[j][i] - c1 - t * c2) + E::to(ev[j].v[i]);
+                dw[j][i] += g * (t * rstd);
+                db[j][i] += g;
             }
             if (at.skip[j] < V) store_vec<E, V>(dx + at.col[j], V, o);
         }
@@ -187,7 +207,7 @@ hipError_t launch(const NormArgs &a, const NormShape &s, hipStream_t st)
     };
     constexpr integral_constant<int, V> width{};
     if (s.width == 1) go(integral_constant<int, 16>{}, integral_constant<int, 1>{}, integral_constant<int, 1>{});
-    else if (s.lanes == 16) go(integral_constant<int, 16>{}, integral_constant<int, 1>{}, width);
+    else if (s.lanes == 16) vecs(integral_constant<int, 16>{}, width);
     else if (s.lanes == 64) vecs(integral_constant<int, 64>{}, width);
     else if (s.lanes == 256) vecs(integral_constant<int, 256>{}, width);
     else vecs(integral_constant<int, 1024>{}, width);
@@ -200,7 +220,8 @@ NormShape layer_norm_grad_shape(int dtype, int d)
 {
     const int v = dtype == CONV2D_DTYPE_F32 ? 4 : 8;
     if (d < v) return {16, 1, 1, true};
-    if (d <= 16 * v) return {16, 1, v, true};
+    for (int n : {1, 2})
+        if (d <= 16 * n * v) return {16, n, v, true};
     for (int lanes : {64, 256, 1024})
         for (int n : {1, 2})
             if (d <= lanes * n * v) return {lanes, n, v, true};

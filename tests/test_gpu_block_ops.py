@@ -362,6 +362,8 @@ NORM = [
     (70, 515, BF16, True, True, True, True), (3, 768, F32, True, True, True, True), (17, 1024, F16, False, False, False, True),
     (9, 2731, F16, False, True, True, True), (40, 4096, BF16, False, True, True, True), (6, 5000, F32, True, True, True, True),
     (3, 8191, BF16, True, True, True, True), (5, 16384, F16, False, True, True, False), (2, 16387, F32, True, True, True, True),
+    (2000, 200, F16, False, True, True, True), (300, 129, BF16, True, True, True, False), (70, 12000, BF16, True, True, True, True),
+    (9, 130, F32, True, True, True, True), (5, 256, BF16, False, True, True, True),
     (3, 33001, BF16, False, True, True, True), (1200, 264, BF16, True, True, True, True),
 ]
 
