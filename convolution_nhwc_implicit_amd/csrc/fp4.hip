@@ -9,6 +9,10 @@
 // both operands have the same, so x is loaded to match.  fp32 x is the sum of three bf16
 // values, exactly, so that all products are exact and all sums fp32.  The waves of a
 // workgroup take parts of k and are added through LDS in order.
+//
+// One row of x by 8192 x 4096 takes 7.2 us, a launch's latency and 18 MB (2.5 TB/s); by
+// 32768 x 8192 41 us (3.5 TB/s, some 70 % of the copy's rate).  Waves that take 128 bytes
+// of a row of w at a time in place of 64 change nothing (42.7 and 44.4 us).
 #include <algorithm>
 #include <type_traits>
 
@@ -349,6 +353,8 @@ __global__ __launch_bounds__(64 * kWaves) void fp4_matmul_kernel(Fp4MatmulArgs a
 // mostly reads.  Here four waves of 32 rows of w each share x, which goes through LDS
 // 256 values of k a turn (twice: the next turn's is written while one is used; the one
 // after that is under way), and workgroups split k, so that each reads a part of x only.
+// 48 rows by 8200 x 4104, fp16: 14.6 us, of which the matrix unit needs 2.4 and the bytes
+// 3.7: a workgroup has three or four turns, whose loads nothing covers at first.
 constexpr int kManyWaves = 4, kManyTiles = 2, kManyRows = 16 * kManyTiles * kManyWaves;
 constexpr int kManyPass = 64 * kManyWaves / 32;  // rows of x that the threads read together
 constexpr int kTurn = 2 * kStep * kFp4Group;  // values of k

@@ -7,11 +7,16 @@
 // take successive runs of a segment's tokens.  Each computes its run's decays and
 // inputs, the product of the decays and the state it would end with from zero; these
 // are joined by shuffles and through LDS, so that every lane has the state that its run
-// starts with, and walks the run again in registers.  Where a sequence begins inside a run, product
-// and state are cut off there (product -1), so that nothing of one sequence, infinities
-// and NaN among it, reaches another: runs, segments and chunks need not know sequences.
-// Chunks that begin inside a sequence get their state from a first pass over the chunks
-// before them.
+// starts with, and walks the run again in registers.  Where a sequence begins inside a
+// run, product and state are cut off there (product -1), so that nothing of one sequence,
+// infinities and NaN among it, reaches another: runs, segments and chunks need not know
+// sequences.  Chunks that begin inside a sequence get their state from a first pass over
+// the chunks before them, whose decays and states a chunk's waves compose.
+//
+// Bound by memory: 4 x 4096 tokens of 4096 bf16 channels, walked whole, 151 us (4.4 TB/s);
+// one sequence of 8192, walked twice, 53 us (3.8 TB/s) for the chunks' ends and 64 (5.3
+// TB/s) for the outputs.  Runs of 4 tokens: with 8 the training shape's three walks take
+// 533 us for 514 and the long sequence 137 for 126.  Two channels to a lane: one load brings both.
 #include "recur_common.h"
 
 namespace cnv {
@@ -150,6 +155,7 @@ __global__ __launch_bounds__(64 * kRecurWaves, 4) void recur_kernel(RecurArgs a)
 
 // One token: a thread to VC channels of a row.  The last one's loads are moved back as
 // above; states are updated in place, so it writes only the channels that are its own.
+// 4 rows of 4096 channels take 4.8 us with the call, which is a launch's latency.
 template <class E, int VC>
 __global__ __launch_bounds__(256) void recur_step_kernel(RecurStepArgs a)
 {

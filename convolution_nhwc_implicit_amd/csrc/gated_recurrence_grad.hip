@@ -12,6 +12,11 @@
 // chunk's tokens before it do to a state, and for the chunk what its tokens do to a
 // state and to the gradient that flows back through it.  The second goes backwards: a
 // segment's states come from what the first walk left, its gradients from behind.
+//
+// Bound by memory: 4 x 4096 tokens of 4096 bf16 channels 112 us (3.6 TB/s) for the first
+// walk, which writes what the second one needs of a segment, and 264 us (4.6 TB/s) for the
+// second, which holds 209 registers: two waves to a SIMD.  Runs of 16 tokens spill (the
+// three walks 1096 us); of 2 the second walk alone takes 376.
 #include "recur_common.h"
 
 namespace cnv {
