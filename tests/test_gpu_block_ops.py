@@ -67,6 +67,8 @@ RECUR = [
     (list(range(64)), True, 258, BF16, True, True, True),
     (list(range(65)), True, 100, F32, True, False, True),
     ([3, 7000, 2, 1500, 1], True, 7, F32, True, True, True),
+    ([1, 0, 2, 1] * 1024, True, 40, BF16, True, True, True),
+    ([0, 1, 1] * 1370, True, 5, F32, True, True, True),
     ([2500], False, 300, F16, True, True, True),
     ([16] * 300, False, 300, BF16, True, True, True),
     ([5] * 300, False, 40, F32, True, True, True),
