@@ -498,16 +498,17 @@ __device__ inline void recur_flow(uint32_t last, bool lasts, const float (&av)[T
     }
 }
 
-// Where sequences begin, every `stride`th a lane: the wave finds a token's sequence among
+// Where sequences begin, every stride()th a lane: the wave finds a token's sequence among
 // up to 64 of them without a load, among up to 4096 with one, where a search waits for a
 // load each time it halves (2000 single tokens of 4096 channels with states take 81 us, by
 // searches 170).
 struct RecurStarts {
-    int v, stride;
-    __device__ inline RecurStarts(const Seqs &q) : v(0), stride((q.seqs + 63) / 64)
+    int v;
+    __device__ inline RecurStarts(const Seqs &q) : v(0)
     {
-        if (q.start && stride <= 64) v = start(q, threadIdx.x % 64 * stride);
+        if (q.start && stride(q) <= 64) v = start(q, threadIdx.x % 64 * stride(q));
     }
+    static __device__ inline int stride(const Seqs &q) { return (q.seqs + 63) / 64; }
     static __device__ inline int start(const Seqs &q, int s) { return s < q.seqs ? (int)q.begin(s) : INT32_MAX; }
     // how many lanes' values are at most t, less one; not below 0 whatever they are
     static __device__ inline int last(int v, int t)
@@ -519,15 +520,16 @@ struct RecurStarts {
     template <class Place>
     __device__ inline int find(const Seqs &q, const Place &at, long long t) const
     {
-        if (!q.start || stride > 64) return q.find(t);
+        const int step = (int)scalar_here(stride(q));
+        if (!q.start || step > 64) return q.find(t);
         int s = 0;
 #pragma unroll
         for (int g = 0; g < Place::Q; ++g) {
             const int tg = __builtin_amdgcn_readlane((int)t, g * (64 / Place::Q));
             int n = last(v, tg);
-            if (stride > 1) {
+            if (step > 1) {
                 const int lane = threadIdx.x % 64;
-                n = n * stride + last(lane < stride ? start(q, n * stride + lane) : INT32_MAX, tg);
+                n = n * step + last(lane < step ? start(q, n * step + lane) : INT32_MAX, tg);
             }
             s = at.q == g ? n : s;
         }
