@@ -14,8 +14,8 @@
 // segment's states come from what the first walk left, its gradients from behind.
 //
 // Bound by memory: 4 x 4096 tokens of 4096 bf16 channels 112 us (3.6 TB/s) for the first
-// walk, which writes what the second one needs of a segment, and 264 us (4.6 TB/s) for the
-// second, which holds 209 registers: two waves to a SIMD.  Runs of 16 tokens spill (the
+// walk, which writes what the second one needs of a segment, and 264 to 280 us (4.3 to 4.6
+// TB/s) for the second, which holds some 200 registers: two waves to a SIMD.  Runs of 16 tokens spill (the
 // three walks 1096 us); of 2 the second walk alone takes 376.
 #include "recur_common.h"
 

@@ -9,7 +9,7 @@
 // each workgroup, and column_sums adds those.  Two sums over the lanes a row: the mean;
 // then the squares around it, g, and g times the distance from the mean together.
 //
-// Bound by memory: 16384 rows of 4096 bf16, with dtotal, 111 us (5.0 TB/s with the
+// Bound by memory: 16384 rows of 4096 bf16, with dtotal, 115 us (4.8 TB/s with the
 // partial sums) and 5 us for their sum.  The next row's loads ahead of the sums changed
 // nothing; rows of two vectors a lane that are turned to fp32 at once spill with 1024
 // lanes (4096 of 16384: 302 us with their sum, as they are 182).
