@@ -89,7 +89,7 @@ bool recur_fits(const gated_recurrence_problem_t *p, const RecurPlan &r)
     return fits((r.chunks + ceil_div(p->batch.seqs, kRecurStateSeqs)) * r.across + 8, 64 * kRecurWaves);
 }
 
-RecurArgs recur_args(const gated_recurrence_problem_t *p, const RecurPlan &r)
+RecurArgs recur_args(const gated_recurrence_problem_t *p, const RecurPlan &r, const void *z)
 {
     RecurArgs a = {};
     a.q = seqs_of(p->batch);
@@ -103,7 +103,8 @@ RecurArgs recur_args(const gated_recurrence_problem_t *p, const RecurPlan &r)
     a.xs = stride_of(p->x);
     a.rs = stride_of(p->r);
     a.is = stride_of(p->i);
-    a.zs = stride_of(p->z);
+    a.z = z;
+    if (z) a.zs = stride_of(p->z);  // else 0: the kernels mark an absent tensor by an offset, which a row's would carry round
     a.dys = stride_of(p->dy);
     return a;
 }
@@ -192,11 +193,10 @@ int gated_recurrence(const gated_recurrence_problem_t *prob, int dtype, const vo
     if (need && !workspace) return CONV2D_ERR_INVALID_ARGUMENT;
     if (workspace_bytes < need) return CONV2D_ERR_WORKSPACE_TOO_SMALL;
     if (!rows && !final_state) return CONV2D_OK;
-    RecurArgs a = recur_args(prob, plan);
+    RecurArgs a = recur_args(prob, plan, z);
     a.x = x;
     a.r = r;
     a.i = i;
-    a.z = z;
     a.A = A;
     a.r_bias = r_bias;
     a.i_bias = i_bias;
@@ -241,11 +241,10 @@ int gated_recurrence_grad(const gated_recurrence_problem_t *prob, int dtype, con
     const size_t need = recur_grad_bytes(prob, plan);
     if (need && !workspace) return CONV2D_ERR_INVALID_ARGUMENT;
     if (workspace_bytes < need) return CONV2D_ERR_WORKSPACE_TOO_SMALL;
-    RecurArgs a = recur_args(prob, plan);
+    RecurArgs a = recur_args(prob, plan, z);
     a.x = x;
     a.r = r;
     a.i = i;
-    a.z = z;
     a.dy = dy;
     a.A = A;
     a.r_bias = r_bias;

@@ -233,7 +233,7 @@ struct RecurRows {
         : base((const char *)p + (a.per_seq ? k.seq * (s.seq - (long long)a.q.len * s.row) * E::kBytes : 0) + k.c0 * s.row * E::kBytes),
           row((uint32_t)s.row * E::kBytes), width((uint32_t)a.d * E::kBytes)
     {
-        run = p ? (uint32_t)(at.q * Place::kRun) * row + (uint32_t)at.c * E::kBytes : kRecurNowhere;  // no tensor: zeros
+        run = p ? (uint32_t)(at.q * Place::kRun) * row + (uint32_t)at.c * E::kBytes : kRecurNowhere;  // no tensor: zeros, at any row (its stride is 0)
     }
     __device__ inline __amdgpu_buffer_rsrc_t span(const RecurSpan &s) const
     {

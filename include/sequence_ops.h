@@ -247,7 +247,7 @@ int fp8_matmul(const fp8_matmul_problem_t *prob, int dtype, const void *a, const
  *   y[t][c] = h[t][c] * silu(z[t][c])
  * with h before a sequence's first token its initial_state, or zero without one.
  *   x, r, i, z  rows of d elements, dtype, with the strides below.  z may be NULL
- *             (y = h).
+ *             (y = h; its strides only have to be valid ones then).
  *   A [d] (log decays, at most 0: growing states are NaN; rates below -2e38 count
  *             as -2e38), r_bias, i_bias [d] (may be NULL: zero), initial_state and
  *             final_state [seqs][d] (may be NULL): fp32, dense.  The states must
