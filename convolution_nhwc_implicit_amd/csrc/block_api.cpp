@@ -255,7 +255,7 @@ int gated_recurrence_grad(const gated_recurrence_problem_t *prob, int dtype, con
     a.dx = g->dx;
     a.dr = g->dr;
     a.di = g->di;
-    a.dz = g->dz;
+    a.dz = z ? g->dz : nullptr;
     Carver w{(char *)workspace};
     a.partial = w.take(up((size_t)plan.chunks * 3 * prob->d * 4));
     a.seg_decay = w.take(plan.per_segment);

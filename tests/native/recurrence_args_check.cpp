@@ -54,6 +54,7 @@ int main()
                 const int e = gated_recurrence_grad(&p, CONV2D_DTYPE_BF16, at, at, at, at, f, z, f, f, f, f, &g, at, (size_t)1 << 40, nullptr);
                 expect(e == CONV2D_OK && launches == 1, "the gradient is refused", seqs, len);
                 expect(seen.z == z && seen.zs.row == (z ? d : 0) && seen.zs.seq == (z ? s.seq : 0), "strides of z, gradient", seqs, len);
+                expect(!seen.dz == !z, "a gradient for z, just where z is there", seqs, len);
                 expect(seen.xs.row == d && seen.rs.row == d && seen.is.row == d && seen.dys.row == d, "strides", seqs, len);
             }
         }

@@ -51,3 +51,15 @@ def test_gradients_without_z_take_any_strides_of_it(seqs, n, d, lens):
     for got in out[1:]:
         assert all(torch.equal(a, b) for a, b in zip(got, out[0]))
     assert all(bool(v.isfinite().all()) for v in out[0]) and bool(out[0][0].any())
+
+
+def test_gradients_without_z_leave_dz_alone():
+    """z NULL and a dz given all the same: nothing is written there."""
+    g = torch.Generator(device=DEV).manual_seed(2)
+    x, r, i, dy = (torch.randn(70, 40, device=DEV, generator=g).to(BF16) for _ in range(4))
+    A, s = -torch.rand(40, device=DEV, generator=g), Stride(40, 2800)
+    p = Recur(Batch(None, 1, 70, 70), 40, s, s, s, s, s)
+    dz = torch.full_like(x, 3.0)
+    got = abi_grads(p, dy, x, r, i, A, dz=dz)
+    assert bool((dz == 3.0).all())
+    assert all(torch.equal(a, b) for a, b in zip(got, abi_grads(p, dy, x, r, i, A)))
