@@ -33,8 +33,13 @@ struct RecurPlan {
     size_t per_chunk, per_segment;  // bytes of a value for each of them and channel
 };
 
-// Whether one stride reaches all rows of a batch.
-bool one_stride(const seq_batch_t &b, const seq_stride_t &s) { return b.seq_start || b.seqs == 1 || s.seq == b.len * s.row; }
+// Whether one stride reaches all rows of a batch.  Of sequences of one token it is that
+// between sequences: such an axis's own stride means nothing, and callers give any.
+bool single_tokens(const seq_batch_t &b) { return !b.seq_start && b.seqs > 1 && b.len == 1; }
+bool one_stride(const seq_batch_t &b, const seq_stride_t &s)
+{
+    return b.seq_start || b.seqs == 1 || (single_tokens(b) ? s.seq <= kMaxStride : s.seq == b.len * s.row);
+}
 
 // Sequences are walked whole where that alone gives every compute unit a workgroup, for
 // chunks are read twice; else they are cut so that each unit has as many workgroups as
@@ -106,6 +111,8 @@ RecurArgs recur_args(const gated_recurrence_problem_t *p, const RecurPlan &r, co
     a.z = z;
     if (z) a.zs = stride_of(p->z);  // else 0: the kernels mark an absent tensor by an offset, which a row's would carry round
     a.dys = stride_of(p->dy);
+    if (!r.per_seq && single_tokens(p->batch))
+        for (RowStride *s : {&a.xs, &a.rs, &a.is, &a.zs, &a.dys}) s->row = s->seq;
     return a;
 }
 

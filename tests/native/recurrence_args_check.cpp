@@ -58,6 +58,28 @@ int main()
                 expect(seen.xs.row == d && seen.rs.row == d && seen.is.row == d && seen.dys.row == d, "strides", seqs, len);
             }
         }
+    // sequences of one token: rows like any others, whatever the stride over the tokens' axis is called
+    for (int seqs : {2, 100, 1024, 150000})
+        for (long long row : {0LL, 4096LL, 8192LL}) {
+            const seq_stride_t s = {row, 4096}, half = {row, 8192};
+            gated_recurrence_problem_t p = {{nullptr, seqs, 1, seqs}, 4096, s, half, half, s, s};
+            float *f = (float *)at;
+            gated_recurrence_grads_t g = {at, at, at, f, at, f, f, f};
+            for (bool grad : {false, true}) {
+                const int r = grad ? gated_recurrence_grad(&p, CONV2D_DTYPE_BF16, at, at, at, at, f, at, f, f, f, f, &g, at, (size_t)1 << 40, nullptr)
+                                   : gated_recurrence(&p, CONV2D_DTYPE_BF16, at, at, at, f, at, f, f, f, at, f, at, (size_t)1 << 40, nullptr);
+                expect(r == CONV2D_OK, "one-token sequences are refused", seqs, 1);
+                expect(!seen.per_seq && seen.xs.row == 4096 && seen.rs.row == 8192 && seen.is.row == 8192 && seen.zs.row == 4096 &&
+                       (!grad || seen.dys.row == 4096), "one-token sequences lie apart", seqs, 1);
+            }
+        }
+    // but for strides that no row may have
+    {
+        const seq_stride_t s = {0, 64}, far = {0, 1LL << 25};
+        gated_recurrence_problem_t p = {{nullptr, 9, 1, 9}, 64, far, s, s, s, s};
+        const int r = gated_recurrence(&p, CONV2D_DTYPE_BF16, at, at, at, (float *)at, at, nullptr, nullptr, nullptr, at, nullptr, at, (size_t)1 << 40, nullptr);
+        expect(r == CONV2D_OK && seen.per_seq == 1 && seen.xs.seq == 1LL << 25 && seen.xs.row == 0, "one-token sequences far apart", 9, 1);
+    }
     if (!bad) printf("ok\n");
     return bad != 0;
 }

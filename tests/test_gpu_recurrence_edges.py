@@ -4,7 +4,10 @@ import ctypes as ct
 import pytest
 import torch
 
+import block_ref as R
+import convolution_nhwc_implicit_amd as nn
 from test_block_cpu import Recur, RecurGrads
+from test_gpu_block_ops import close, recur_call, recur_case, recur_grads, recur_ref, same_but_for_chunks
 from test_sequence_cpu import BF16C, LIB, OK, Batch, Stride, size
 
 pytestmark = pytest.mark.gpu
@@ -63,3 +66,62 @@ def test_gradients_without_z_leave_dz_alone():
     got = abi_grads(p, dy, x, r, i, A, dz=dz)
     assert bool((dz == 3.0).all())
     assert all(torch.equal(a, b) for a, b in zip(got, abi_grads(p, dy, x, r, i, A)))
+
+
+# ------------------------------------------------------------------------- dense batches of one-token sequences
+NAMES = dict(x="dx", r="dr", i="di", A="dA", z="dz", rb="dr_bias", ib="di_bias", init="dinitial_state")
+
+
+@pytest.mark.parametrize("seqs,d,typ,states", [(2, 3, F32, True), (5, 70, BF16, True), (300, 131, F16, True), (1024, 256, BF16, False),
+                                               (700, 520, F32, True)], ids=str)
+def test_one_token_sequences(seqs, d, typ, states):
+    lens = [1] * seqs
+    c, p, lead, _ = recur_case((lens, False, d, typ, True, True, states))  # each tensor with a stride of its own
+    y, final = recur_call(p, None, state=True)
+    v, (wy, wf, ey, ef) = recur_ref(c, lens, grad=True)
+    close(y[:, 0], wy, ey.detach(), typ, "y")
+    close(final, wf, ef.detach(), F32, "final state")
+    got = recur_grads(p, None)
+    out = (wy * v["dy"]).sum() + (0 if v["dfinal"] is None else (wf * v["dfinal"]).sum())
+    have = [k for k in NAMES if v[k] is not None]
+    want = torch.autograd.grad(out, [v[k] for k in have])
+    with torch.no_grad():
+        bound = R.recurrence_grad_bounds(v["dy"], *(v[k] for k in ("x", "r", "i", "A", "z", "rb", "ib")), lens, v["init"], v["dfinal"])
+    for k, w in zip(have, want):
+        n = NAMES[k]
+        close(got[n].reshape(w.shape), w, bound[n], typ if n in ("dx", "dr", "di", "dz") else F32, n)
+
+
+def test_one_token_sequences_of_a_projection_and_of_one_row():
+    """Both gates as halves of one product's output, and one row of x for all sequences; against the same rows packed."""
+    g = torch.Generator(device=DEV).manual_seed(4)
+    seqs, d = 900, 264
+    gates, z, dy = (torch.randn(seqs, 1, k * d, device=DEV, generator=g).to(BF16) for k in (2, 1, 1))
+    r, i = gates.split(d, -1)
+    A, h0 = -torch.rand(d, device=DEV, generator=g), torch.randn(seqs, d, device=DEV, generator=g)
+    one = torch.randn(1, 1, d, device=DEV, generator=g).to(BF16).expand(seqs, 1, d)
+    start = torch.arange(seqs + 1, dtype=torch.int32, device=DEV)
+    for x in (z.flip(0), one):
+        kw = dict(z=z, initial_state=h0)
+        flat = dict(z=z[:, 0], initial_state=h0, seq_start=start)
+        y, f = nn.gated_recurrence(x, r, i, A, return_state=True, **kw)
+        wy, wf = nn.gated_recurrence(x[:, 0], r[:, 0], i[:, 0], A, return_state=True, **flat)
+        assert same_but_for_chunks(y[:, 0], wy) and same_but_for_chunks(f, wf)
+        k = nn.gated_recurrence_grad(dy, x, r, i, A, **kw)
+        w = nn.gated_recurrence_grad(dy[:, 0], x[:, 0], r[:, 0], i[:, 0], A, **flat)
+        assert all(same_but_for_chunks(k[n].reshape(w[n].shape), w[n]) for n in ("dx", "dr", "di", "dz", "dinitial_state"))
+        # 900 terms of size 1, each with some tens of roundings
+        assert float((k["dA"] - w["dA"]).abs().max()) <= 900 * 64 * R.U
+
+
+def test_one_token_sequences_far_apart():
+    """The last tokens of long sequences, whose distance no row stride may have."""
+    g = torch.Generator(device=DEV).manual_seed(5)
+    wide = torch.randn(5, (1 << 25) // 64, 64, device=DEV, generator=g).to(BF16)
+    x, r, i = (wide[:, -k:][:, :1] for k in (1, 2, 3))
+    A = -torch.rand(64, device=DEV, generator=g)
+    y = nn.gated_recurrence(x, r, i, A)
+    assert same_but_for_chunks(y, nn.gated_recurrence(x.contiguous(), r.contiguous(), i.contiguous(), A))
+    k = nn.gated_recurrence_grad(x, x, r, i, A)
+    w = nn.gated_recurrence_grad(x.contiguous(), x.contiguous(), r.contiguous(), i.contiguous(), A)
+    assert all(same_but_for_chunks(k[n], w[n]) for n in ("dx", "dr", "di"))
