@@ -3,9 +3,10 @@
 // With L = A g, b = sqrt(1 - a^2) u x, G = dy silu(z) and k the gradient of a state:
 //   k = G + (what flows in from the next token);  flows on: a k
 //   dx = k sqrt(1 - a^2) u;  di = k b (1 - u);  dz = dy h silu'(z)
-//   dL = k (a h_before - a^2 / sqrt(1 - a^2) u x);  dr = dL L (1 - g);  dA = sum dL g
-// dL L is what is computed: L / sqrt(1 - a^2) goes to 0 with L, where the root's own
-// derivative has no bound; dA is the sum of dL L over A.
+//   dL = k (a h_before - a^2 / (1 - a^2) b);  dr = dL L (1 - g);  dA = sum dL g
+// dL L is what is computed: L / (1 - a^2) goes to -1/2 with L, where the quotient alone has
+// no bound; dA is the sum of dL L over A.  1 - g and 1 - u come from the gates' exponentials:
+// as differences they would be off by 2^-24, whatever their size.
 //
 // Two walks over each chunk, in segments whose waves take successive runs as in the
 // forward pass.  The first goes forwards and leaves, for every segment, what the
@@ -191,9 +192,7 @@ __global__ __launch_bounds__(64 * kRecurWaves) void recur_grad_kernel(RecurArgs 
     const Tensors<E, VC> in(a, chunk, at);
     const RecurOut<E, VC> dxr(a.dx, a, chunk, at), drr(a.dr, a, chunk, at), dir(a.di, a, chunk, at), dzr(a.dz, a, chunk, at);
     const bool gate = a.z;
-    float invA[VC], dll[VC] = {}, drb[VC] = {}, dib[VC] = {};
-#pragma unroll
-    for (int v = 0; v < VC; ++v) invA[v] = ch.A[v] == 0.0f ? 0.0f : 1.0f / ch.A[v];
+    float dll[VC] = {}, drb[VC] = {}, dib[VC] = {};
     const int segs = (chunk.len + kSegment - 1) / kSegment;
     Raw xs[T], rs[T], is[T], zs[T], ds[T];
     struct {
@@ -241,17 +240,17 @@ __global__ __launch_bounds__(64 * kRecurWaves) void recur_grad_kernel(RecurArgs 
         recur_get<VC>(a.seg_decay, k0, a.d, at.c, until.dec);
         recur_get<VC>(a.seg_state, k0, a.d, at.c, until.end);
         aim(RecurSpan(chunk, at, seg > 0 ? seg + lead - kSegment : segs * kSegment));
-        // su: sqrt(1 - a^2) u; hv: the inputs, then the states before the tokens; qv: dz by h
-        float Lv[T][VC], av[T][VC], su[T][VC], hv[T][VC], gv[T][VC], qv[T][VC];
+        // su: sqrt(1 - a^2) u; rest, shut: 1 - g, 1 - u; hv: the inputs, then the states before the tokens; qv: dz by h
+        float Lv[T][VC], av[T][VC], su[T][VC], rest[T][VC], shut[T][VC], hv[T][VC], gv[T][VC], qv[T][VC];
         Raw x[T];
 #pragma unroll
         for (int j = 0; j < T; ++j) {
             x[j] = xs[j];
 #pragma unroll
             for (int v = 0; v < VC; ++v) {
-                Lv[j][v] = ch.A[v] * recur_gate(rs[j][v], ch.rb[v]);
+                Lv[j][v] = ch.A[v] * recur_gate(rs[j][v], ch.rb[v], rest[j][v]);
                 av[j][v] = __builtin_amdgcn_exp2f(Lv[j][v]);
-                su[j][v] = __builtin_amdgcn_sqrtf(one_minus_square(Lv[j][v], av[j][v])) * recur_gate(is[j][v], ch.ib[v]);
+                su[j][v] = __builtin_amdgcn_sqrtf(one_minus_square(Lv[j][v], av[j][v])) * recur_gate(is[j][v], ch.ib[v], shut[j][v]);
                 hv[j][v] = su[j][v] * x[j][v];
                 const float dy = ds[j][v];
                 const float z = zs[j][v], s = sigmoid_f32(z);
@@ -310,13 +309,13 @@ __global__ __launch_bounds__(64 * kRecurWaves) void recur_grad_kernel(RecurArgs 
 #pragma unroll
             for (int v = 0; v < VC; ++v) {
                 const float L = Lv[j][v], dec = av[j][v], xx = x[j][v], b = su[j][v] * xx;
-                // 1 / sqrt(1 - a^2), finite where a is 1: it meets L or b there, which are 0
-                const float root = __builtin_amdgcn_rsqf(fmaxf(one_minus_square(L, dec), 1.2e-38f)), u = su[j][v] * root;
+                // L / (1 - a^2) by an inverse that is finite where a is 1: it meets L and b there, which are 0
+                const float ratio = L * __builtin_amdgcn_rcpf(fmaxf(one_minus_square(L, dec), 1.2e-38f));
                 if (!INSIDE) k[v] = run.last >> j & 1 ? 0.0f : k[v];
                 k[v] += gv[j][v];
-                const float dl = kLn2 * k[v] * (L * dec * hv[j][v] - (L * root) * (dec * dec) * (u * xx));  // dL * L
-                orr[v] = dl * (1.0f - L * invA[v]);
-                oi[v] = k[v] * b * (1.0f - u);
+                const float dl = kLn2 * k[v] * (L * dec * hv[j][v] - ratio * dec * (dec * b));  // dL * L; a first, which is 0 for the largest L
+                orr[v] = dl * rest[j][v];
+                oi[v] = k[v] * b * shut[j][v];
                 ox[v] = k[v] * su[j][v];
                 oz[v] = qv[j][v] * fmaf(dec, hv[j][v], b);
                 dll[v] += dl;

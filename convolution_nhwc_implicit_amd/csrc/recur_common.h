@@ -34,6 +34,14 @@ __device__ inline float recur_gate(float v, float b)
 {
     return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(fmaf(v, -kLog2e, b)));
 }
+// and what it leaves of 1, to as many bits of its own: 1 / (1 + e) and e / (1 + e)
+__device__ inline float recur_gate(float v, float b, float &rest)
+{
+    const float e = __builtin_amdgcn_exp2f(fmaf(v, -kLog2e, b)), g = __builtin_amdgcn_rcpf(1.0f + e);
+    rest = __builtin_amdgcn_fmed3f(e * g, 0.0f, 1.0f);  // a number where e is infinite and g 0; what it meets is 0 with g
+    asm("" : "+v"(rest));  // now: until it is used, e and g would take two registers
+    return g;
+}
 
 // 1 - a^2 for a = 2^L, L <= 0.  Near 1 the difference would lose a's last bits: above L = -1/2,
 // where a^2 is 1/2, a polynomial in L in its place, whose first coefficient is -2 ln 2 and the

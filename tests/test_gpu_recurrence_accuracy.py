@@ -38,3 +38,47 @@ def test_inputs_scale_of_all_decays(lo, hi):
     want = torch.sqrt(-torch.expm1(2 * A.double()))
     assert float(((y - want) / want).abs().max()) <= 7 * R.U
     assert float(((dx - want) / want).abs().max()) <= 7 * R.U
+
+
+@pytest.mark.parametrize("typ", [F16, BF16, F32], ids=str)
+def test_gradients_of_open_and_shut_gates(typ):
+    """dr and di of gates near 0 and 1, relative to themselves: a gate times its complement, both of which a sigmoid has
+    to all its bits. One term each, in which no sum cancels:
+      dr = -k a^2 / s u x A g (1 - g),  di = k s x u (1 - u)
+    A sigmoid or a complement is off by (8 + 4 |v|) U relative, a^2 / s by 32 U and (8 + 4 |r|) |L| U, ten products by U
+    each; below fp32's normal numbers nothing is left (a complement of 2^-126 times terms of at most 2^6)."""
+    g = torch.Generator().manual_seed(3)
+    v = torch.tensor([-INF, -100.0, -20.0, -8.0, -1.0, 0.0, 1.0, 4.0, 8.0, 12.0, 16.0, 20.0, 60.0, 100.0, INF])
+    r, i = torch.cartesian_prod(v, v).t()
+    d = 12
+    A = -torch.exp2(torch.linspace(-8, 1, d))
+    r, i = (t[:, None].expand(-1, d).to(typ).contiguous() for t in (r, i))
+    x, dy = (torch.randn(r.shape, generator=g).to(typ) for _ in range(2))
+    got = call(nn.gated_recurrence_grad, dy, x, r, i, A)
+    xd, dyd, rd, id_, Ad = (t.double() for t in (x, dy, r, i, A))
+    gate, take = torch.sigmoid(rd), torch.sigmoid(id_)
+    gate[gate < 2.0 ** -126] = 0  # as documented: their root, some 2^-72, is gone with them
+    L = Ad * gate
+    s = torch.sqrt(-torch.expm1(2 * L))
+    want = dict(dr=-dyd * torch.exp(2 * L) / s.clamp_min(1e-300) * take * xd * L * torch.sigmoid(-rd),
+                di=dyd * s * xd * take * torch.sigmoid(-id_))
+    vr, vi = (t.abs().clamp_max(128) for t in (rd, id_))  # infinite gates are exact
+    count = 64 + 12 * vr + 8 * vi + (8 + 4 * vr) * L.abs()
+    for k, w in want.items():
+        tol = (count * R.U + R.half_step(typ)) * w.abs() + 2.0 ** -120 + torch.finfo(typ).smallest_normal * torch.finfo(typ).eps
+        off = (got[k].double().cpu() - w).abs()
+        assert bool((off <= tol).all()), (k, float((off / tol).max()))
+    assert not got["dr"][(r == INF).to(DEV)].any() and not got["di"][(i == INF).to(DEV)].any()
+
+
+def test_bias_gradients_of_open_gates_vanish():
+    """Fully open gates: 4000 tokens leave nothing in the biases' gradients, and nothing of one sign at 30."""
+    g = torch.Generator().manual_seed(4)
+    t, d = 4000, 70
+    x, dy = (torch.randn(t, d, generator=g).to(DEV) for _ in range(2))
+    A, b = -torch.rand(d, generator=g).to(DEV) - 0.01, torch.zeros(d, device=DEV)
+    for v, most in ((INF, 0.0), (100.0, 0.0), (30.0, t * 2.0 ** -40)):
+        gate = torch.full_like(x, v)
+        k = nn.gated_recurrence_grad(dy, x, gate, gate, A, r_bias=b, i_bias=b)
+        # sums of t terms of a few times e^-30 = 2^-43.3 each; e^-100 is below the normal numbers
+        assert float(k["dr_bias"].abs().max()) <= most + 2.0 ** -110 and float(k["di_bias"].abs().max()) <= most + 2.0 ** -110
