@@ -19,7 +19,8 @@ RecurrentBlock, a gated linear recurrence behind a norm, on a residual stream:
 
 The projections are fp8 products with a scale for every 128 values: weights are quantised once in blocks of
 128 x 128, both as they are and transposed (for the inputs' gradients), activations and gradients by rows in each
-call. Blocks made with four_bit=True hold 4-bit weights too, a scale for every 32 values, for their single tokens.
+call. Blocks made with four_bit=True hold 4-bit weights too, a scale for every 32 values, for their single tokens
+(block.four_bit, by name: new weights are quantised anew for both).
 """
 import torch
 
@@ -55,21 +56,28 @@ class Fp4Linear:
         return S.fp4_matmul(x, *self.w)
 
 
-def _projections(block, weights, names, four_bit):
-    """Fp8Linear of each weight on the block, and by name those that its single tokens take."""
-    for k in names:
-        setattr(block, k, Fp8Linear(weights[k]))
-    return {k: Fp4Linear(weights[k]) if four_bit else getattr(block, k) for k in names}
+class _Block:
+    def _project(self, weights, names, four_bit):
+        """Fp8Linear of each weight on the block, and 4-bit ones beside them if asked for."""
+        self.projections = names
+        for k in names:
+            setattr(self, k, Fp8Linear(weights[k]))
+        self.four_bit = {k: Fp4Linear(weights[k]) for k in names} if four_bit else {}
+
+    @property
+    def token(self):
+        """The projections that single tokens take, by name: the 4-bit ones, or those that everything else takes."""
+        return {k: self.four_bit.get(k) or getattr(self, k) for k in self.projections}
 
 
-class GatedBlock:
+class GatedBlock(_Block):
     """Weights in float32: in_proj [2d][model], conv [d][w], conv_bias [d], x_proj [d + 2 groups n][d],
     dt_bias [d], A [d][n] (negative), D [d], out_proj [model][d]."""
 
     def __init__(self, weights, groups=1, dtype=torch.bfloat16, four_bit=False):
         self.d, self.n = weights["A"].shape
         self.groups, self.dtype = groups, dtype
-        self.token = _projections(self, weights, ("in_proj", "x_proj", "out_proj"), four_bit)
+        self._project(weights, ("in_proj", "x_proj", "out_proj"), four_bit)
         self.conv, self.conv_bias = weights["conv"].to(dtype), weights["conv_bias"].to(dtype)
         self.A, self.D, self.dt_bias = (weights[k].float().contiguous() for k in ("A", "D", "dt_bias"))
 
@@ -141,7 +149,7 @@ class GatedBlock:
         return out, g
 
 
-class RecurrentBlock:
+class RecurrentBlock(_Block):
     """Weights in float32: norm, norm_bias [model], in_proj [2d][model], conv [d][w], conv_bias [d], gate_proj [2d][d],
     r_bias, i_bias [d], A [d] (negative), out_proj [model][d].
 
@@ -149,7 +157,7 @@ class RecurrentBlock:
 
     def __init__(self, weights, dtype=torch.bfloat16, eps=1e-5, four_bit=False):
         self.d, self.dtype, self.eps = weights["A"].shape[0], dtype, eps
-        self.token = _projections(self, weights, ("in_proj", "gate_proj", "out_proj"), four_bit)
+        self._project(weights, ("in_proj", "gate_proj", "out_proj"), four_bit)
         self.conv, self.conv_bias = weights["conv"].to(dtype), weights["conv_bias"].to(dtype)
         self.norm, self.norm_bias, self.A, self.r_bias, self.i_bias = (
             weights[k].float().contiguous() for k in ("norm", "norm_bias", "A", "r_bias", "i_bias"))

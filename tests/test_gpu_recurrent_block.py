@@ -6,7 +6,7 @@ import torch
 import block_ref as B
 import sequence_ref as R
 from convolution_nhwc_implicit_amd import gated_block
-from convolution_nhwc_implicit_amd.gated_block import Fp4Linear, GatedBlock, RecurrentBlock
+from convolution_nhwc_implicit_amd.gated_block import Fp4Linear, Fp8Linear, GatedBlock, RecurrentBlock
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -112,3 +112,26 @@ def test_both_blocks_on_one_stream():
 def test_command(capsys):
     gated_block.main()
     assert capsys.readouterr().out.count("training step") == 2
+
+
+@pytest.mark.parametrize("kind", ["gated", "recurrent"])
+def test_tokens_take_a_projection_that_was_replaced(kind):
+    """New weights on a block, as after a training step: single tokens take them too."""
+    def block():
+        gen = torch.Generator(device=DEV).manual_seed(9)
+        return GatedBlock.random(128, 192, 16, generator=gen) if kind == "gated" else RecurrentBlock.random(128, 192, generator=gen)
+
+    gen = torch.Generator(device=DEV).manual_seed(10)
+    one = block()
+    u = torch.randn(5, 128, device=DEV, generator=gen).to(torch.bfloat16)
+    weight = torch.randn(128, 192, device=DEV, generator=gen) * 192 ** -0.5
+
+    def step(b):
+        y = b.step(u, b.states(5))
+        return y if kind == "gated" else y[0]
+
+    before = step(one)
+    one.out_proj = Fp8Linear(-weight)
+    after = step(one)
+    one.out_proj = Fp8Linear(weight)
+    assert torch.equal(step(one), -after) and not torch.equal(after, before)
