@@ -13,6 +13,7 @@ from test_sequence_cpu import BF16C, LIB, OK, Batch, Stride, size
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
 F16, BF16, F32 = torch.float16, torch.bfloat16, torch.float32
+INF = float("inf")
 
 
 def at(t):
@@ -125,3 +126,37 @@ def test_one_token_sequences_far_apart():
     k = nn.gated_recurrence_grad(x, x, r, i, A)
     w = nn.gated_recurrence_grad(x.contiguous(), x.contiguous(), r.contiguous(), i.contiguous(), A)
     assert all(same_but_for_chunks(k[n], w[n]) for n in ("dx", "dr", "di"))
+
+
+# --------------------------------------------------------------------------------------- single tokens without slots
+@pytest.mark.parametrize("rows,pool,d,typ,gate", [(1, 3, 1, F32, True), (4, 9, 130, BF16, True), (7, 7, 4097, F16, False),
+                                                  (300, 400, 256, BF16, True), (33, 40, 6, F32, True)], ids=str)
+def test_step_without_slots(rows, pool, d, typ, gate):
+    """Row r takes and leaves state r, every other state stays as it is."""
+    c, _, _, _ = recur_case(([1] * rows, True, d, typ, gate, True, True), seed=6)
+    state = torch.randn(pool, d, generator=torch.Generator().manual_seed(7))
+    c["init"] = state[:rows]
+    _, (wy, wf, ey, ef) = recur_ref(c, [1] * rows)
+    held = state.to(DEV)
+    t = {k: None if v is None else v.to(DEV) for k, v in c.items()}
+    y = nn.gated_recurrence_step(t["x"], t["r"], t["i"], t["A"], held, z=t["z"], r_bias=t["rb"], i_bias=t["ib"])
+    close(y, wy, ey, typ, "y")
+    close(held[:rows], wf, ef, F32, "states")
+    assert torch.equal(held[rows:].cpu(), state[rows:])
+    again = state.to(DEV)
+    slots = torch.arange(rows, dtype=torch.int32, device=DEV)
+    same = nn.gated_recurrence_step(t["x"], t["r"], t["i"], t["A"], again, z=t["z"], r_bias=t["rb"], i_bias=t["ib"], slots=slots)
+    assert torch.equal(same, y) and torch.equal(again, held)
+
+
+@pytest.mark.parametrize("typ", [F16, BF16, F32], ids=str)
+def test_growing_states_are_nan(typ):
+    """A above 0: NaN where the gate is open at all, in results and gradients; other channels as ever."""
+    g = torch.Generator(device=DEV).manual_seed(8)
+    x, r, i, dy = (torch.randn(2, 200, 6, device=DEV, generator=g).to(typ) for _ in range(4))
+    A = torch.tensor([-0.5, 1e-30, 0.01, 3.0, INF, -0.5], device=DEV)
+    y, f = nn.gated_recurrence(x, r, i, A, return_state=True)
+    k = nn.gated_recurrence_grad(dy, x, r, i, A)
+    assert bool(y[..., 1:5].isnan().all()) and bool(f[:, 1:5].isnan().all())
+    assert all(bool(k[n][..., 1:5].isnan().all()) for n in ("dx", "dr", "di", "dA"))
+    assert all(bool(k[n][..., [0, 5]].isfinite().all()) for n in ("dx", "dr", "di", "dA")) and bool(y[..., [0, 5]].isfinite().all())
