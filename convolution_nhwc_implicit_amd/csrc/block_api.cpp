@@ -44,11 +44,11 @@ bool one_stride(const seq_batch_t &b, const seq_stride_t &s)
 // Sequences are walked whole where that alone gives every compute unit a workgroup, for
 // chunks are read twice; else they are cut so that each unit has as many workgroups as
 // it holds: two in the forward pass, one in the gradient's.  (8192 tokens of 4096 bf16
-// channels: forward 132 us with two, 139 with one; 3 x 517 of 768, gradients: 48 us with
-// one, 58 with two.)  Whole sequences give a workgroup 128 bytes of a row (with 64 and
-// twice the workgroups the training step of 4 x 4096 x 4096 takes 730 us instead of 530),
-// cut ones, which can make up for it by shorter chunks, 256: the 8192 tokens' walk to
-// the outputs takes 63 us, 5.3 TB/s, with 128 it took 73.
+// channels: forward 102 us with two, 114 with one; gradients 230 with one, 228 with two, but
+// of 3001 packed tokens of 1999 channels with states 58 and 62.)  Whole sequences give a
+// workgroup 128 bytes of a row (with 64 and twice the workgroups 4 x 4096 x 4096 takes 188 us
+// instead of 150, its gradients 457 instead of 370), cut ones, which can make up for it by
+// shorter chunks, 256: the 8192 tokens take 102 us, with 128 bytes 119.
 // Chunks run over all tokens, sequences' borders inside them, unless a dense batch's
 // sequences lie apart.
 RecurPlan recur_plan(const gated_recurrence_problem_t *p, int dtype, bool grad)

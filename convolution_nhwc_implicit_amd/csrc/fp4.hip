@@ -85,7 +85,8 @@ struct AsParts {
 
 // Whether fp16 cannot hold e2m1 values with this scale, 0.5 * 2^-23 to 6 * 2^13.  The scale
 // of a group of zeros, 2^-127, does not count: whatever it scales, times any fp16 value, is
-// nothing to an fp16 sum.
+// nothing to an fp16 sum.  A workgroup that meets such a scale walks all of k again with x in two
+// parts: with one among the weights 1 x 8192 x 4096 takes 15 us for 8, 48 x 8200 x 4104 68 for 17.
 __device__ inline bool too_wide(uint32_t e) { return e - 104u > 36u && e != 0; }
 
 // eight e2m1 values in 16 bits, times the power of two whose exponent field is scale's

@@ -13,10 +13,11 @@
 // sequences.  Chunks that begin inside a sequence get their state from a first pass over
 // the chunks before them, whose decays and states a chunk's waves compose.
 //
-// Bound by memory: 4 x 4096 tokens of 4096 bf16 channels, walked whole, 151 us (4.4 TB/s);
-// one sequence of 8192, walked twice, 53 us (3.8 TB/s) for the chunks' ends and 64 (5.3
-// TB/s) for the outputs.  Runs of 4 tokens: with 8 the training shape's three walks take
-// 533 us for 514 and the long sequence 137 for 126.  Two channels to a lane: one load brings both.
+// Bound by memory: 4 x 4096 tokens of 4096 bf16 channels, walked whole, 150 us (4.5 TB/s);
+// one sequence of 8192, walked twice, 52 us (3.9 TB/s) for the chunks' ends and 63 (5.3
+// TB/s) for the outputs.  Runs of 4 tokens: with 2 the batch takes 176 us and the long
+// sequence 117 (with 4 both walks 102), with 8, whose values no longer fit the registers of
+// four waves to a SIMD, 281 and 176.  Two channels to a lane: one load brings both.
 #include "recur_common.h"
 
 namespace cnv {

@@ -14,10 +14,10 @@
 // state and to the gradient that flows back through it.  The second goes backwards: a
 // segment's states come from what the first walk left, its gradients from behind.
 //
-// Bound by memory: 4 x 4096 tokens of 4096 bf16 channels 112 us (3.6 TB/s) for the first
-// walk, which writes what the second one needs of a segment, and 264 to 280 us (4.3 to 4.6
-// TB/s) for the second, which holds some 200 registers: two waves to a SIMD.  Runs of 16 tokens spill (the
-// three walks 1096 us); of 2 the second walk alone takes 376.
+// Bound by memory: 4 x 4096 tokens of 4096 bf16 channels 109 us (3.7 TB/s) for the first
+// walk, which writes what the second one needs of a segment, and 262 us (4.6 TB/s) for the
+// second, which holds some 200 registers: two waves to a SIMD.  Runs of 8 tokens spill
+// (both walks 1127 us for 370); with 2 they take 493.
 #include "recur_common.h"
 
 namespace cnv {

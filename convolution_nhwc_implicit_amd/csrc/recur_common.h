@@ -185,7 +185,7 @@ struct RecurRun {
 // token and end with its last one that is there: tokens past it are not read (but where
 // rows overlap) and not written, without branches, and a lane needs one 32-bit offset
 // for a tensor.
-constexpr uint32_t kRecurNowhere = 0xfffffff0u;  // past every range: 63 rows of 2^26 bytes and one's elements
+constexpr uint32_t kRecurNowhere = 0xfffffff0u;  // past every range: at most 31 rows of 2^26 bytes and one's elements
 
 __device__ inline __amdgpu_buffer_rsrc_t recur_buffer(const void *p, uint32_t bytes)
 {

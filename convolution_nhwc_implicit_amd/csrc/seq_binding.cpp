@@ -735,7 +735,6 @@ struct Norm {
         const size_t n = x->dim();
         const int64_t seqs = n == 3 ? x->size(0) : 1, len = x->size(n - 2);
         p = {int_size(seqs, "sequences"), int_size(len, "tokens"), int_size(d, "d"), (float)e, strides(*x), {0, 0}, {0, 0}, {0, 0}};
-        // rows that one stride reaches need no sequences
         if (seqs * len > INT32_MAX) value_error("there are at most 2^31 - 1 rows");
     }
     seq_stride_t strides(const Tensor &t) const
